@@ -27,6 +27,9 @@ EXPORTED = (
     # shared expert (moe_shared.h)
     "moe_shared_workspace_size", "moe_get_shared_workspace_layout", "moe_shared_ffn",
     "moe_finalize_shared", "moe_forward_shared",
+    # router gradients (moe_router_grad.h)
+    "moe_balance_workspace_size", "moe_balance_loss", "moe_route_backward",
+    "moe_router_grad_workspace_size", "moe_router_weight_grad", "moe_finalize_backward",
     # measurement probes (moe_probe.h)
     "moe_probe_mfma_bf16", "moe_probe_mfma_flops", "moe_probe_read",
 )
@@ -91,6 +94,18 @@ def _load():
     lib.moe_finalize_shared.restype = i32
     lib.moe_forward_shared.argtypes = [S, i32, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     lib.moe_forward_shared.restype = i32
+    lib.moe_balance_workspace_size.argtypes = [S]
+    lib.moe_balance_workspace_size.restype = ctypes.c_size_t
+    lib.moe_balance_loss.argtypes = [S, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.moe_balance_loss.restype = i32
+    lib.moe_route_backward.argtypes = [S, P, P, P, P, P, P, P, P, P]
+    lib.moe_route_backward.restype = i32
+    lib.moe_router_grad_workspace_size.argtypes = [S]
+    lib.moe_router_grad_workspace_size.restype = ctypes.c_size_t
+    lib.moe_router_weight_grad.argtypes = [S, P, P, P, P, P, P, ctypes.c_size_t, P]
+    lib.moe_router_weight_grad.restype = i32
+    lib.moe_finalize_backward.argtypes = [S, P, P, P, P, P]
+    lib.moe_finalize_backward.restype = i32
     lib.moe_probe_mfma_bf16.argtypes = [i32, P, P]
     lib.moe_probe_mfma_bf16.restype = i32
     lib.moe_probe_mfma_flops.argtypes = [i32]
@@ -321,6 +336,72 @@ def moe_forward_shared(shape, Is, x, wg, bias, w1, w2, w1s, w2s, out, workspace,
                                   _arg("w1s", w1s, dt, 2 * Is * H), _arg("w2s", w2s, dt, H * Is),
                                   _arg("out", out, dt, T * H), ws, nbytes, _stream(stream)),
            "moe_forward_shared")
+
+
+# ---- router gradients (moe_router_grad.h)
+
+
+def _on_current(*tensors):
+    """The library launches on the current device: every tensor has to be on it."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.device.index != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+
+
+def moe_balance_workspace_size(shape: MoeShape) -> int:
+    return int(lib.moe_balance_workspace_size(ctypes.byref(shape)))
+
+
+def moe_balance_loss(shape, logits, topk_ids, token_mask, counts, mean_prob, loss, workspace, stream=None):
+    """Per-expert counts, mean router probabilities and the balance loss of the valid tokens."""
+    T, E, k = shape.T, shape.E, shape.k
+    args = (_arg("logits", logits, torch.float32, T * E), _arg("topk_ids", topk_ids, torch.int32, T * k),
+            _arg("token_mask", token_mask, torch.uint8, T, nullable=True), _arg("counts", counts, torch.int32, E),
+            _arg("mean_prob", mean_prob, torch.float32, E), _arg("loss", loss, torch.float32, 1))
+    ws, nbytes = _workspace(workspace)
+    _on_current(logits, topk_ids, token_mask, counts, mean_prob, loss, workspace)
+    _check(lib.moe_balance_loss(ctypes.byref(shape), *args, ws, nbytes, _stream(stream)), "moe_balance_loss")
+
+
+def moe_route_backward(shape, logits, topk_ids, topk_w, token_mask, counts, d_topk_w, d_loss, d_logits, stream=None):
+    """Gradient of the router logits from those of the routing weights and of the balance loss (either may be None)."""
+    T, E, k = shape.T, shape.E, shape.k
+    args = (_arg("logits", logits, torch.float32, T * E), _arg("topk_ids", topk_ids, torch.int32, T * k),
+            _arg("topk_w", topk_w, torch.float32, T * k),
+            _arg("token_mask", token_mask, torch.uint8, T, nullable=True),
+            _arg("counts", counts, torch.int32, E, nullable=True),
+            _arg("d_topk_w", d_topk_w, torch.float32, T * k, nullable=True),
+            _arg("d_loss", d_loss, torch.float32, 1, nullable=True),
+            _arg("d_logits", d_logits, torch.float32, T * E))
+    _on_current(logits, topk_ids, topk_w, token_mask, counts, d_topk_w, d_loss, d_logits)
+    _check(lib.moe_route_backward(ctypes.byref(shape), *args, _stream(stream)), "moe_route_backward")
+
+
+def moe_router_grad_workspace_size(shape: MoeShape) -> int:
+    return int(lib.moe_router_grad_workspace_size(ctypes.byref(shape)))
+
+
+def moe_router_weight_grad(shape, x, d_logits, token_mask, d_wg, d_bias, workspace, stream=None):
+    """Gradients of the router's weight and (unless d_bias is None) bias."""
+    T, H, E = shape.T, shape.H, shape.E
+    args = (_arg("x", x, _layer_dtype(shape), T * H), _arg("d_logits", d_logits, torch.float32, T * E),
+            _arg("token_mask", token_mask, torch.uint8, T, nullable=True),
+            _arg("d_wg", d_wg, torch.float32, E * H), _arg("d_bias", d_bias, torch.float32, E, nullable=True))
+    ws, nbytes = _workspace(workspace)
+    _on_current(x, d_logits, token_mask, d_wg, d_bias, workspace)
+    _check(lib.moe_router_weight_grad(ctypes.byref(shape), *args, ws, nbytes, _stream(stream)),
+           "moe_router_weight_grad")
+
+
+def moe_finalize_backward(shape, y, inv, d_out, d_topk_w, stream=None):
+    """Gradient of the routing weights from the output's (y as the down projection wrote it)."""
+    T, H, k = shape.T, shape.H, shape.k
+    R = T * k
+    args = (_arg_bytes("y", y, y_nbytes(shape, R)), _arg("inv", inv, torch.int32, R),
+            _arg("d_out", d_out, _layer_dtype(shape), T * H), _arg("d_topk_w", d_topk_w, torch.float32, R))
+    _on_current(y, inv, d_out, d_topk_w)
+    _check(lib.moe_finalize_backward(ctypes.byref(shape), *args, _stream(stream)), "moe_finalize_backward")
 
 
 def moe_probe_mfma_bf16(iterations: int, sink, stream=None) -> float:

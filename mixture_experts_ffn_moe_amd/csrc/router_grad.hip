@@ -1,0 +1,628 @@
+// What the router is trained with: balance loss and per-expert counts, the
+// gradient of the logits, of the routing weights, and of the router's weight.
+// Formulas and argument semantics: moe_router_grad.h.
+//
+// Everything here streams its inputs once.  Sums over tokens run in a fixed
+// order (per-workgroup partials in the workspace, then one summing pass), so
+// no result depends on the order of atomics.
+#include "../../include/moe_router_grad.h"
+#include "api_check.h"
+
+#include <algorithm>
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Softmax of four tokens per wave: 16 lanes per token, lane l of them holding
+// experts l, l + 16, l + 32, l + 48.  A token then needs four-step reductions
+// over 16 lanes, shared by the wave's four tokens (one token per wave, one
+// lane per expert, would take six steps for each token alone).
+constexpr int kTokWave = 4;
+constexpr int kPer = kMaxExperts / 16;  // experts per lane
+
+template <typename F>
+__device__ __forceinline__ float row16_reduce(float v, F f) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) v = f(v, __shfl_xor(v, d));
+  return v;
+}
+__device__ __forceinline__ float row16_sum(float v) {
+  return row16_reduce(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ float row16_max(float v) {
+  return row16_reduce(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// Probabilities of the token whose logits start at `row`, 0 past E and for a
+// row that is not `ok` (its values are loaded from a valid address and dropped).
+__device__ __forceinline__ void softmax16(const float (&v)[kPer], int l, int E, bool ok, float (&p)[kPer]) {
+  float m = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) m = fmaxf(m, l + 16 * i < E ? v[i] : -INFINITY);
+  m = row16_max(m);
+  if (m == -INFINITY) m = 0.0f;  // no finite logit: every exponential below is 0
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    p[i] = l + 16 * i < E ? expf(v[i] - m) : 0.0f;
+    s += p[i];
+  }
+  s = row16_sum(s);
+  const float r = s > 0.0f ? 1.0f / s : 0.0f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) p[i] = ok ? p[i] * r : 0.0f;
+}
+
+// ---------------------------------------------------------------------------
+// Balance loss.  One workgroup of 16 waves takes 64 tokens a step and a
+// contiguous run of tokens in all; its sums go to the workspace in fp64, and
+// a second launch of one workgroup adds them (one workgroup alone finishes by
+// itself).
+constexpr int kBalWaves = 16;
+constexpr int kBalStep = kBalWaves * kTokWave;  // tokens per step of a workgroup
+constexpr int kBalBlocks = 256;                 // at most one workgroup per CU
+
+struct BalancePartial {
+  double prob[kMaxExperts];
+  int32_t count[kMaxExperts];
+  int32_t valid;
+  int32_t pad[15];
+};
+
+__device__ __forceinline__ void balance_write(double prob, int count, int n, int E, int k, int lane,
+                                              int32_t* __restrict__ counts, float* __restrict__ mean_prob,
+                                              float* __restrict__ loss) {
+  const double mean = n > 0 ? prob / (double)n : 0.0;
+  const double f = n > 0 ? (double)count / ((double)n * k) : 0.0;
+  double s = lane < E ? f * mean : 0.0;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) s += __shfl_xor(s, d);
+  if (lane < E) {
+    counts[lane] = count;
+    mean_prob[lane] = (float)mean;
+  }
+  if (lane == 0) loss[0] = (float)(E * s);
+}
+
+__global__ __launch_bounds__(kBalWaves * 64) void balance_partial(
+    const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask, int T,
+    int E, int k, int per_block, BalancePartial* __restrict__ partial, int32_t* __restrict__ counts,
+    float* __restrict__ mean_prob, float* __restrict__ loss) {
+  __shared__ double prob[kBalWaves][kMaxExperts];
+  __shared__ int hcnt[kMaxExperts + 1];  // counts, then the number of valid tokens
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l = lane & 15, g = lane >> 4;
+  const int t_begin = blockIdx.x * per_block, t_end = min(T, t_begin + per_block);
+  if (tid <= kMaxExperts) hcnt[tid] = 0;
+  __syncthreads();
+
+  double sum[kPer] = {};
+  int valid = 0;
+  for (int t0 = t_begin; t0 < t_end; t0 += kBalStep) {
+    const int t = t0 + wave * kTokWave + g;
+    const int tc = min(t, t_end - 1);
+    const bool ok = t < t_end && (mask == nullptr || mask[tc] != 0);
+    float v[kPer], p[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) v[i] = logits[(size_t)tc * E + min(l + 16 * i, E - 1)];
+    softmax16(v, l, E, ok, p);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum[i] += (double)p[i];
+    valid += (ok && l == 0) ? 1 : 0;
+  }
+  for (int r = t_begin * k + tid; r < t_end * k; r += kBalWaves * 64) {
+    const int e = ids[r];
+    if ((mask == nullptr || mask[r / k] != 0) && (unsigned)e < (unsigned)E) atomicAdd(&hcnt[e], 1);
+  }
+  // the wave's four tokens of a step, then the 16 waves, in a fixed order
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    double d = sum[i];
+    d += __shfl_xor(d, 16);
+    d += __shfl_xor(d, 32);
+    if (g == 0) prob[wave][l + 16 * i] = d;
+  }
+  if (l == 0 && valid > 0) atomicAdd(&hcnt[kMaxExperts], valid);
+  __syncthreads();
+  if (wave != 0) return;
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kBalWaves; ++w) s += prob[w][lane];
+  if (gridDim.x == 1) {
+    balance_write(s, hcnt[lane], hcnt[kMaxExperts], E, k, lane, counts, mean_prob, loss);
+    return;
+  }
+  BalancePartial& out = partial[blockIdx.x];
+  out.prob[lane] = s;
+  out.count[lane] = hcnt[lane];
+  if (lane == 0) out.valid = hcnt[kMaxExperts];
+}
+
+__global__ __launch_bounds__(kBalWaves * 64) void balance_finish(const BalancePartial* __restrict__ partial, int nb,
+                                                                 int E, int k, int32_t* __restrict__ counts,
+                                                                 float* __restrict__ mean_prob,
+                                                                 float* __restrict__ loss) {
+  __shared__ double prob[kBalWaves][kMaxExperts];
+  __shared__ int cnt[kBalWaves][kMaxExperts], val[kBalWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double s = 0.0;
+  int c = 0, n = 0;
+  for (int b = wave; b < nb; b += kBalWaves) {
+    s += partial[b].prob[lane];
+    c += partial[b].count[lane];
+    n += partial[b].valid;
+  }
+  prob[wave][lane] = s;
+  cnt[wave][lane] = c;
+  if (lane == 0) val[wave] = n;
+  __syncthreads();
+  if (wave != 0) return;
+  s = 0.0;
+  c = 0;
+  n = 0;
+#pragma unroll
+  for (int w = 0; w < kBalWaves; ++w) {
+    s += prob[w][lane];
+    c += cnt[w][lane];
+    n += val[w];
+  }
+  balance_write(s, c, n, E, k, lane, counts, mean_prob, loss);
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the logits: 16 lanes per token as above.  The routes' values
+// are scattered to the experts through an LDS row per token (written and read
+// by the token's own wave).
+constexpr int kRbWaves = 4;
+
+__global__ __launch_bounds__(kRbWaves * 64) void route_backward(
+    const float* __restrict__ logits, const int32_t* __restrict__ ids, const float* __restrict__ topw,
+    const uint8_t* __restrict__ mask, const int32_t* __restrict__ counts, const float* __restrict__ d_w,
+    const float* __restrict__ d_loss, int T, int E, int k, int renorm, float* __restrict__ d_logits) {
+  __shared__ float sel[kRbWaves][kTokWave][kMaxExperts];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l = lane & 15, g = lane >> 4;
+  float* row = sel[wave][g];
+
+  // f[e] of this lane's experts and the loss's coefficient d_loss * E / N
+  float f[kPer] = {}, coef = 0.0f;
+  if (d_loss != nullptr) {
+    const int ce = lane < E ? counts[lane] : 0;
+    int total = ce;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) total += __shfl_xor(total, d);
+    const float fe = total > 0 ? (float)((double)ce / (double)total) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) f[i] = __shfl(fe, l + 16 * i);
+    coef = total > 0 ? (float)((double)d_loss[0] * E * k / (double)total) : 0.0f;
+  }
+  const bool need_p = d_loss != nullptr || !renorm;
+
+  for (int t0 = blockIdx.x * kRbWaves * kTokWave; t0 < T; t0 += gridDim.x * kRbWaves * kTokWave) {
+    const int t = t0 + wave * kTokWave + g;
+    const int tc = min(t, T - 1);
+    const bool ok = t < T && (mask == nullptr || mask[tc] != 0);
+    float p[kPer] = {}, d[kPer] = {};
+    if (need_p) {
+      float v[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) v[i] = logits[(size_t)tc * E + min(l + 16 * i, E - 1)];
+      softmax16(v, l, E, ok, p);
+      float fp = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) fp = fmaf(f[i], p[i], fp);
+      fp = row16_sum(fp);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) d[i] = coef * p[i] * (f[i] - fp);
+    }
+    if (d_w != nullptr) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) row[l + 16 * i] = 0.0f;
+      float dot = 0.0f;
+      for (int j = l; j < k; j += 16) {
+        const size_t r = (size_t)tc * k + j;
+        dot = fmaf(topw[r], d_w[r], dot);
+      }
+      dot = row16_sum(dot);
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      for (int j = l; j < k; j += 16) {
+        const size_t r = (size_t)tc * k + j;
+        const int e = ids[r];
+        if ((unsigned)e < (unsigned)E) row[e] = renorm ? topw[r] * (d_w[r] - dot) : d_w[r];
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const float s = row[l + 16 * i];
+        d[i] += renorm ? s : p[i] * (s - dot);
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+    if (t < T) {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (l + 16 * i < E) d_logits[(size_t)t * E + l + 16 * i] = ok ? d[i] : 0.0f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the routing weights: one workgroup per token, as the finalize
+// whose backward pass it is; d_out's row is read once per eight routes, each
+// thread taking 8 columns (one y block) of d_out and of eight rows of y.
+constexpr int kFbThreads = 256;
+constexpr int kFbRoutes = 8;
+
+__device__ __forceinline__ void load_cols8(const uint16_t* p, float (&v)[8]) {
+  const uint4 r = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load_cols8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+// dot of 8 columns of one y row with d
+__device__ __forceinline__ float ydot8(const float* y, const int8_t*, size_t row, int H, int c, const float (&d)[8]) {
+  float v[8], s = 0.0f;
+  load_cols8(y + row * H + c, v);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s = fmaf(v[q], d[q], s);
+  return s;
+}
+__device__ __forceinline__ float ydot8(const _Float16* y, const int8_t* ye, size_t row, int H, int c,
+                                       const float (&d)[8]) {
+  typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+  const f16x8 h = *reinterpret_cast<const f16x8*>(y + row * H + c);
+  const int e = ye[row * ((H + kYBlock - 1) / kYBlock) + c / kYBlock];
+  float s = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) s = fmaf((float)h[q], d[q], s);
+  return ldexpf(s, e);
+}
+
+// NJ routes [j0, j0 + NJ) of token t (NJ known to the compiler: the NJ row
+// loads of a step are all in flight before the first is used).
+template <int NJ, typename T, typename YT>
+__device__ __forceinline__ void finalize_backward_routes(const YT* __restrict__ y, const int8_t* __restrict__ ye,
+                                                         const int32_t* __restrict__ inv,
+                                                         const T* __restrict__ d_out, int H,
+                                                         float (&part)[kFbThreads / 64][kFbRoutes],
+                                                         float* __restrict__ d_w) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  size_t rows[NJ];
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) rows[j] = (size_t)inv[j];
+  float acc[NJ] = {};
+  for (int c = tid * 8; c < H; c += kFbThreads * 8) {
+    float d[8];
+    load_cols8(d_out + c, d);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[j] += ydot8(y, ye, rows[j], H, c, d);
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; ++j) {
+#pragma unroll
+    for (int s = 1; s < kWave; s <<= 1) acc[j] += __shfl_xor(acc[j], s);
+    if (lane == 0) part[wave][j] = acc[j];
+  }
+  __syncthreads();
+  if (tid < NJ) {
+    float s = part[0][tid];
+#pragma unroll
+    for (int w = 1; w < kFbThreads / 64; ++w) s += part[w][tid];
+    d_w[tid] = s;
+  }
+  __syncthreads();
+}
+
+template <typename T, typename YT>
+__global__ __launch_bounds__(kFbThreads) void finalize_backward(const YT* __restrict__ y,
+                                                                const int8_t* __restrict__ ye,
+                                                                const int32_t* __restrict__ inv,
+                                                                const T* __restrict__ d_out, int H, int k,
+                                                                float* __restrict__ d_w) {
+  __shared__ float part[kFbThreads / 64][kFbRoutes];
+  const int t = blockIdx.x;
+  inv += (size_t)t * k;
+  d_w += (size_t)t * k;
+  d_out += (size_t)t * H;
+  int j = 0;
+  for (; j + 8 <= k; j += 8) finalize_backward_routes<8>(y, ye, inv + j, d_out, H, part, d_w + j);
+  if (k & 4) {
+    finalize_backward_routes<4>(y, ye, inv + j, d_out, H, part, d_w + j);
+    j += 4;
+  }
+  if (k & 2) {
+    finalize_backward_routes<2>(y, ye, inv + j, d_out, H, part, d_w + j);
+    j += 2;
+  }
+  if (k & 1) finalize_backward_routes<1>(y, ye, inv + j, d_out, H, part, d_w + j);
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the router's weight on v_mfma_f32_16x16x4_f32: a lane supplies
+// one token's (k = lane/16) d_logits of expert 16 mt + lane%16 as A and one
+// token's x column as B, so both operands are taken as they lie in memory.  A
+// lane loads four neighbouring columns 4 (lane%16) + q; column tile q then
+// holds columns q, q + 4, ..., and a lane's four results of a row are
+// neighbours again.  A workgroup covers 64 experts x 64 columns over one run
+// of tokens, its 16 waves taking every 16th step of 4 tokens; the waves' sums
+// are added through LDS in a fixed order.
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+constexpr int kWgWaves = 16;
+constexpr int kWgCols = 64;
+constexpr int kWgBlocks = 256;    // workgroups aimed at
+constexpr int kWgMinTokens = 64;  // fewest tokens worth a workgroup of their own
+
+inline int wgrad_splits(int T, int H) {
+  return std::max(1, std::min(kWgBlocks / (H / kWgCols), (T + kWgMinTokens - 1) / kWgMinTokens));
+}
+
+__device__ __forceinline__ f32x4v load_cols4(const uint16_t* p) {
+  const uint2 r = *reinterpret_cast<const uint2*>(p);
+  return f32x4v{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
+                __uint_as_float(r.y & 0xffff0000u)};
+}
+__device__ __forceinline__ f32x4v load_cols4(const float* p) { return *reinterpret_cast<const f32x4v*>(p); }
+
+// part: [splits][64][H] then [splits][64] bias sums; one split writes the results themselves
+template <typename XT>
+__global__ __launch_bounds__(kWgWaves * 64) void router_weight_grad(
+    const XT* __restrict__ x, const float* __restrict__ dl, const uint8_t* __restrict__ mask, int T, int H, int E,
+    int per_split, float* __restrict__ part, float* __restrict__ bias_part, float* __restrict__ d_wg,
+    float* __restrict__ d_bias) {
+  __shared__ float red[kWgWaves / 2][kMaxExperts][kWgCols];
+  __shared__ float bred[kWgWaves][kMaxExperts];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l = lane & 15, g = lane >> 4;
+  const int split = blockIdx.y, h0 = blockIdx.x * kWgCols;
+  const int t_begin = split * per_split, t_end = min(T, t_begin + per_split);
+  f32x4v acc[4][4];
+  float bsum[4] = {};
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[m][q] = f32x4v{0.f, 0.f, 0.f, 0.f};
+
+  for (int t0 = t_begin + wave * 4; t0 < t_end; t0 += kWgWaves * 4) {
+    const int t = t0 + g, tc = min(t, t_end - 1);
+    const bool ok = t < t_end && (mask == nullptr || mask[tc] != 0);
+    f32x4v b = load_cols4(x + (size_t)tc * H + h0 + 4 * l);
+    float a[4];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int e = 16 * m + l;
+      const float v = dl[(size_t)tc * E + min(e, E - 1)];
+      a[m] = ok && e < E ? v : 0.0f;
+      bsum[m] += a[m];
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) b[q] = ok ? b[q] : 0.0f;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[m][q] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[m], b[q], acc[m][q], 0, 0, 0);
+  }
+  // D layout: register r of a lane holds row 4 (lane/16) + r, column lane%16
+#pragma unroll
+  for (int half = kWgWaves / 2; half >= 1; half >>= 1) {
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<f32x4v*>(&red[wave - half][16 * m + 4 * g + r][4 * l]) =
+              f32x4v{acc[m][0][r], acc[m][1][r], acc[m][2][r], acc[m][3][r]};
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4v o = *reinterpret_cast<const f32x4v*>(&red[wave][16 * m + 4 * g + r][4 * l]);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[m][q][r] += o[q];
+        }
+    }
+    __syncthreads();
+  }
+  const bool last = gridDim.y == 1;
+  if (wave == 0) {
+    float* out = last ? d_wg : part + (size_t)split * kMaxExperts * H;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int e = 16 * m + 4 * g + r;
+        if (e < E)
+          *reinterpret_cast<f32x4v*>(out + (size_t)e * H + h0 + 4 * l) =
+              f32x4v{acc[m][0][r], acc[m][1][r], acc[m][2][r], acc[m][3][r]};
+      }
+  }
+  if (blockIdx.x != 0) return;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    float v = bsum[m];
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    if (g == 0) bred[wave][16 * m + l] = v;
+  }
+  __syncthreads();
+  if (tid < kMaxExperts) {
+    float s = bred[0][tid];
+#pragma unroll
+    for (int w = 1; w < kWgWaves; ++w) s += bred[w][tid];
+    if (!last)
+      bias_part[split * kMaxExperts + tid] = s;
+    else if (d_bias != nullptr && tid < E)
+      d_bias[tid] = s;
+  }
+}
+
+// Sum of the splits, ascending; one thread per four columns.
+__global__ __launch_bounds__(256) void router_weight_sum(const float* __restrict__ part,
+                                                         const float* __restrict__ bias_part, int splits, int H,
+                                                         int E, float* __restrict__ d_wg, float* __restrict__ d_bias) {
+  const int i = blockIdx.x * 256 + threadIdx.x, n4 = E * H / 4;
+  if (i < n4) {
+    f32x4v s = f32x4v{0.f, 0.f, 0.f, 0.f};
+    for (int p = 0; p < splits; ++p) s += reinterpret_cast<const f32x4v*>(part + (size_t)p * kMaxExperts * H)[i];
+    reinterpret_cast<f32x4v*>(d_wg)[i] = s;
+  }
+  if (d_bias != nullptr && blockIdx.x == 0 && threadIdx.x < E) {
+    float s = 0.0f;
+    for (int p = 0; p < splits; ++p) s += bias_part[p * kMaxExperts + threadIdx.x];
+    d_bias[threadIdx.x] = s;
+  }
+}
+
+// T == 0: the sums over no tokens.
+__global__ __launch_bounds__(256) void zero_words(uint32_t* a, size_t na, uint32_t* b, size_t nb, uint32_t* c,
+                                                  size_t nc) {
+  const size_t i = blockIdx.x * (size_t)256 + threadIdx.x;
+  if (i < na) a[i] = 0u;
+  if (b != nullptr && i < nb) b[i] = 0u;
+  if (c != nullptr && i < nc) c[i] = 0u;
+}
+
+inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+inline int balance_blocks(int T) { return std::max(1, std::min(kBalBlocks, ceil_div(T, kBalStep))); }
+
+inline size_t wgrad_workspace(const Shape& s) {
+  const size_t sp = (size_t)wgrad_splits(s.T, s.H);
+  return sp == 1 ? 256 : sp * kMaxExperts * ((size_t)s.H + 1) * 4;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe_api;
+
+namespace {
+
+moe_status check_workspace(const void* workspace, size_t have, size_t need) {
+  if (workspace == nullptr || have < need) return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)workspace & (kAlign - 1)) != 0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_balance_workspace_size(const moe_shape* shape) {
+  Shape s;
+  if (check_shape(shape, &s) != MOE_OK) return 0;
+  return align_up((size_t)moe::balance_blocks(s.T) * sizeof(moe::BalancePartial));
+}
+
+moe_status moe_balance_loss(const moe_shape* shape, const float* logits, const int32_t* topk_ids,
+                            const uint8_t* token_mask, int32_t* counts, float* mean_prob, float* loss,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  Shape s;
+  MOE_CHECK(check_shape(shape, &s));
+  MOE_CHECK(check_ptr(counts)); MOE_CHECK(check_ptr(mean_prob)); MOE_CHECK(check_ptr(loss));
+  hipStream_t st = (hipStream_t)stream;
+  if (s.T == 0) {
+    hipLaunchKernelGGL(moe::zero_words, dim3(1), dim3(256), 0, st, (uint32_t*)counts, (size_t)s.E,
+                       (uint32_t*)mean_prob, (size_t)s.E, (uint32_t*)loss, (size_t)1);
+    return hip_status(hipGetLastError());
+  }
+  MOE_CHECK(check_ptr(logits)); MOE_CHECK(check_ptr(topk_ids));
+  if (token_mask != nullptr) MOE_CHECK(check_ptr(token_mask));
+  MOE_CHECK(check_workspace(workspace, workspace_bytes, moe_balance_workspace_size(shape)));
+  const int nb = moe::balance_blocks(s.T);
+  moe::BalancePartial* part = (moe::BalancePartial*)workspace;
+  hipLaunchKernelGGL(moe::balance_partial, dim3(nb), dim3(moe::kBalWaves * 64), 0, st, logits, topk_ids, token_mask,
+                     s.T, s.E, s.k, moe::ceil_div(s.T, nb), part, counts, mean_prob, loss);
+  if (nb > 1)
+    hipLaunchKernelGGL(moe::balance_finish, dim3(1), dim3(moe::kBalWaves * 64), 0, st, part, nb, s.E, s.k, counts,
+                       mean_prob, loss);
+  return hip_status(hipGetLastError());
+}
+
+moe_status moe_route_backward(const moe_shape* shape, const float* logits, const int32_t* topk_ids,
+                              const float* topk_w, const uint8_t* token_mask, const int32_t* counts,
+                              const float* d_topk_w, const float* d_loss, float* d_logits, void* stream) {
+  Shape s;
+  MOE_CHECK(check_shape(shape, &s));
+  if (s.T == 0) return MOE_OK;
+  if (d_topk_w == nullptr && d_loss == nullptr) return MOE_ERR_INVALID_ARG;
+  MOE_CHECK(check_ptr(logits)); MOE_CHECK(check_ptr(topk_ids)); MOE_CHECK(check_ptr(topk_w));
+  MOE_CHECK(check_ptr(d_logits));
+  if (token_mask != nullptr) MOE_CHECK(check_ptr(token_mask));
+  if (d_topk_w != nullptr) MOE_CHECK(check_ptr(d_topk_w));
+  if (d_loss != nullptr) { MOE_CHECK(check_ptr(d_loss)); MOE_CHECK(check_ptr(counts)); }
+  const int blocks = std::min(2048, moe::ceil_div(s.T, moe::kRbWaves * moe::kTokWave));
+  hipLaunchKernelGGL(moe::route_backward, dim3(blocks), dim3(moe::kRbWaves * 64), 0, (hipStream_t)stream, logits,
+                     topk_ids, topk_w, token_mask, counts, d_topk_w, d_loss, s.T, s.E, s.k, (int)s.renorm, d_logits);
+  return hip_status(hipGetLastError());
+}
+
+size_t moe_router_grad_workspace_size(const moe_shape* shape) {
+  Shape s;
+  if (check_shape(shape, &s) != MOE_OK) return 0;
+  return align_up(moe::wgrad_workspace(s));
+}
+
+moe_status moe_router_weight_grad(const moe_shape* shape, const void* x, const float* d_logits,
+                                  const uint8_t* token_mask, float* d_wg, float* d_bias, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  Shape s;
+  MOE_CHECK(check_shape(shape, &s));
+  MOE_CHECK(check_ptr(d_wg));
+  if (d_bias != nullptr) MOE_CHECK(check_ptr(d_bias));
+  hipStream_t st = (hipStream_t)stream;
+  if (s.T == 0) {
+    const size_t n = (size_t)s.E * s.H;
+    hipLaunchKernelGGL(moe::zero_words, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, (uint32_t*)d_wg, n,
+                       (uint32_t*)d_bias, (size_t)s.E, (uint32_t*)nullptr, (size_t)0);
+    return hip_status(hipGetLastError());
+  }
+  MOE_CHECK(check_ptr(x)); MOE_CHECK(check_ptr(d_logits));
+  if (token_mask != nullptr) MOE_CHECK(check_ptr(token_mask));
+  MOE_CHECK(check_workspace(workspace, workspace_bytes, moe_router_grad_workspace_size(shape)));
+  const int splits = moe::wgrad_splits(s.T, s.H);
+  const int per = moe::ceil_div(s.T, splits);
+  float* part = (float*)workspace;
+  float* bpart = part + (size_t)splits * moe::kMaxExperts * s.H;
+  const dim3 grid(s.H / moe::kWgCols, splits), block(moe::kWgWaves * 64);
+  if (s.bf16)
+    hipLaunchKernelGGL(moe::router_weight_grad<uint16_t>, grid, block, 0, st, (const uint16_t*)x, d_logits, token_mask,
+                       s.T, s.H, s.E, per, part, bpart, d_wg, d_bias);
+  else
+    hipLaunchKernelGGL(moe::router_weight_grad<float>, grid, block, 0, st, (const float*)x, d_logits, token_mask, s.T,
+                       s.H, s.E, per, part, bpart, d_wg, d_bias);
+  if (splits > 1)
+    hipLaunchKernelGGL(moe::router_weight_sum, dim3(moe::ceil_div(s.E * s.H / 4, 256)), dim3(256), 0, st, part, bpart,
+                       splits, s.H, s.E, d_wg, d_bias);
+  return hip_status(hipGetLastError());
+}
+
+moe_status moe_finalize_backward(const moe_shape* shape, const void* y, const int32_t* inv, const void* d_out,
+                                 float* d_topk_w, void* stream) {
+  Shape s;
+  MOE_CHECK(check_shape(shape, &s));
+  if (s.T == 0) return MOE_OK;
+  MOE_CHECK(check_ptr(y)); MOE_CHECK(check_ptr(inv)); MOE_CHECK(check_ptr(d_out)); MOE_CHECK(check_ptr(d_topk_w));
+  hipStream_t st = (hipStream_t)stream;
+  if (s.bf16)
+    hipLaunchKernelGGL((moe::finalize_backward<uint16_t, _Float16>), dim3(s.T), dim3(moe::kFbThreads), 0, st,
+                       (const _Float16*)y, (const int8_t*)y + (size_t)s.R() * s.H * 2, inv, (const uint16_t*)d_out,
+                       s.H, s.k, d_topk_w);
+  else
+    hipLaunchKernelGGL((moe::finalize_backward<float, float>), dim3(s.T), dim3(moe::kFbThreads), 0, st,
+                       (const float*)y, (const int8_t*)nullptr, inv, (const float*)d_out, s.H, s.k, d_topk_w);
+  return hip_status(hipGetLastError());
+}
+
+}  // extern "C"

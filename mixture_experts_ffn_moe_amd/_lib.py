@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_PKG, "libmoe_mi355x.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(5)
 MOE_F32, MOE_BF16 = 0, 1
+MOE_Q4_INT4, MOE_Q4_E2M1 = 0, 1
 
 EXPORTED = (
     "moe_status_string", "moe_workspace_size", "moe_get_workspace_layout", "moe_route",
@@ -27,6 +28,9 @@ EXPORTED = (
     # shared expert (moe_shared.h)
     "moe_shared_workspace_size", "moe_get_shared_workspace_layout", "moe_shared_ffn",
     "moe_finalize_shared", "moe_forward_shared",
+    # 4-bit expert weights (moe_q4.h)
+    "moe_q4_get_sizes", "moe_q4_quantize_w13", "moe_q4_quantize_down", "moe_q4_w13_swiglu",
+    "moe_q4_down", "moe_forward_q4",
     # router gradients (moe_router_grad.h)
     "moe_balance_workspace_size", "moe_balance_loss", "moe_route_backward",
     "moe_router_grad_workspace_size", "moe_router_weight_grad", "moe_finalize_backward",
@@ -55,6 +59,14 @@ class MoeWorkspaceLayout(ctypes.Structure):
 
 class MoeSharedLayout(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("hs", "ys", "total")]
+
+
+class MoeQ4Spec(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class MoeQ4Sizes(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_size_t) for n in ("w1_codes", "w1_scales", "w2_codes", "w2_scales")]
 
 
 def _load():
@@ -94,6 +106,16 @@ def _load():
     lib.moe_finalize_shared.restype = i32
     lib.moe_forward_shared.argtypes = [S, i32, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     lib.moe_forward_shared.restype = i32
+    Q = ctypes.POINTER(MoeQ4Spec)
+    lib.moe_q4_get_sizes.argtypes = [S, Q, ctypes.POINTER(MoeQ4Sizes)]
+    lib.moe_q4_quantize_w13.argtypes = [S, Q, P, P, P, P]
+    lib.moe_q4_quantize_down.argtypes = [S, Q, P, P, P, P]
+    lib.moe_q4_w13_swiglu.argtypes = [S, Q, P, P, P, P, P, P, P]
+    lib.moe_q4_down.argtypes = [S, Q, P, P, P, P, P, P]
+    lib.moe_forward_q4.argtypes = [S, Q, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
+    for f in (lib.moe_q4_get_sizes, lib.moe_q4_quantize_w13, lib.moe_q4_quantize_down, lib.moe_q4_w13_swiglu,
+              lib.moe_q4_down, lib.moe_forward_q4):
+        f.restype = i32
     lib.moe_balance_workspace_size.argtypes = [S]
     lib.moe_balance_workspace_size.restype = ctypes.c_size_t
     lib.moe_balance_loss.argtypes = [S, P, P, P, P, P, P, P, ctypes.c_size_t, P]
@@ -338,15 +360,85 @@ def moe_forward_shared(shape, Is, x, wg, bias, w1, w2, w1s, w2s, out, workspace,
            "moe_forward_shared")
 
 
-# ---- router gradients (moe_router_grad.h)
-
-
 def _on_current(*tensors):
     """The library launches on the current device: every tensor has to be on it."""
     here = torch.cuda.current_device()
     for t in tensors:
         if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.device.index != here:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+
+
+# ---- 4-bit expert weights (moe_q4.h)
+
+
+def make_q4(format="int4", group=128) -> MoeQ4Spec:
+    """A 4-bit weight format: "int4" or "e2m1", `group` columns per scale (32, 64 or 128)."""
+    return MoeQ4Spec({"int4": MOE_Q4_INT4, "e2m1": MOE_Q4_E2M1, MOE_Q4_INT4: MOE_Q4_INT4, MOE_Q4_E2M1: MOE_Q4_E2M1}[format], group)
+
+
+def moe_q4_get_sizes(shape, q4) -> dict:
+    """Bytes of the stored 4-bit weights of a layer."""
+    z = MoeQ4Sizes()
+    _check(lib.moe_q4_get_sizes(ctypes.byref(shape), ctypes.byref(q4), ctypes.byref(z)), "moe_q4_get_sizes")
+    return {n: int(getattr(z, n)) for n, _ in MoeQ4Sizes._fields_}
+
+
+def moe_q4_quantize_w13(shape, q4, w1, codes, scales, stream=None):
+    """Quantise w1 [mu, E, 2*Im, H] (layer dtype) into 4-bit storage."""
+    z = moe_q4_get_sizes(shape, q4)
+    args = (_arg("w1", w1, _layer_dtype(shape), shape.micro_count * shape.E * 2 * shape.Im * shape.H),
+            _arg_bytes("codes", codes, z["w1_codes"]), _arg_bytes("scales", scales, z["w1_scales"]))
+    _on_current(w1, codes, scales)
+    _check(lib.moe_q4_quantize_w13(ctypes.byref(shape), ctypes.byref(q4), *args, _stream(stream)),
+           "moe_q4_quantize_w13")
+
+
+def moe_q4_quantize_down(shape, q4, w2, codes, scales, stream=None):
+    """Quantise w2 [mu, E, H, Im] (layer dtype) into 4-bit storage."""
+    z = moe_q4_get_sizes(shape, q4)
+    args = (_arg("w2", w2, _layer_dtype(shape), shape.micro_count * shape.E * shape.H * shape.Im),
+            _arg_bytes("codes", codes, z["w2_codes"]), _arg_bytes("scales", scales, z["w2_scales"]))
+    _on_current(w2, codes, scales)
+    _check(lib.moe_q4_quantize_down(ctypes.byref(shape), ctypes.byref(q4), *args, _stream(stream)),
+           "moe_q4_quantize_down")
+
+
+def moe_q4_w13_swiglu(shape, q4, x, perm, offsets, w1_codes, w1_scales, h, stream=None):
+    T, H, E, R = shape.T, shape.H, shape.E, shape.T * shape.k
+    dt, z = _layer_dtype(shape), moe_q4_get_sizes(shape, q4)
+    args = (_arg("x", x, dt, T * H), _arg("perm", perm, torch.int32, R), _arg("offsets", offsets, torch.int32, E + 1),
+            _arg_bytes("w1_codes", w1_codes, z["w1_codes"]), _arg_bytes("w1_scales", w1_scales, z["w1_scales"]),
+            _arg("h", h, dt, R * shape.micro_count * shape.Im))
+    _on_current(x, perm, offsets, w1_codes, w1_scales, h)
+    _check(lib.moe_q4_w13_swiglu(ctypes.byref(shape), ctypes.byref(q4), *args, _stream(stream)), "moe_q4_w13_swiglu")
+
+
+def moe_q4_down(shape, q4, h, offsets, w2_codes, w2_scales, y, stream=None):
+    E, R = shape.E, shape.T * shape.k
+    z = moe_q4_get_sizes(shape, q4)
+    args = (_arg("h", h, _layer_dtype(shape), R * shape.micro_count * shape.Im),
+            _arg("offsets", offsets, torch.int32, E + 1), _arg_bytes("w2_codes", w2_codes, z["w2_codes"]),
+            _arg_bytes("w2_scales", w2_scales, z["w2_scales"]), _arg_bytes("y", y, y_nbytes(shape, R)))
+    _on_current(h, offsets, w2_codes, w2_scales, y)
+    _check(lib.moe_q4_down(ctypes.byref(shape), ctypes.byref(q4), *args, _stream(stream)), "moe_q4_down")
+
+
+def moe_forward_q4(shape, q4, x, wg, bias, w1_codes, w1_scales, w2_codes, w2_scales, out, workspace, stream=None):
+    """moe_forward over 4-bit expert weights."""
+    T, H, E = shape.T, shape.H, shape.E
+    dt, z = _layer_dtype(shape), moe_q4_get_sizes(shape, q4)
+    args = (_arg("x", x, dt, T * H), _arg("wg", wg, torch.float32, E * H),
+            _arg("gate_bias", bias, torch.float32, E, nullable=True),
+            _arg_bytes("w1_codes", w1_codes, z["w1_codes"]), _arg_bytes("w1_scales", w1_scales, z["w1_scales"]),
+            _arg_bytes("w2_codes", w2_codes, z["w2_codes"]), _arg_bytes("w2_scales", w2_scales, z["w2_scales"]),
+            _arg("out", out, dt, T * H))
+    ws, nbytes = _workspace(workspace)
+    _on_current(x, wg, bias, w1_codes, w1_scales, w2_codes, w2_scales, out, workspace)
+    _check(lib.moe_forward_q4(ctypes.byref(shape), ctypes.byref(q4), *args, ws, nbytes, _stream(stream)),
+           "moe_forward_q4")
+
+
+# ---- router gradients (moe_router_grad.h)
 
 
 def moe_balance_workspace_size(shape: MoeShape) -> int:

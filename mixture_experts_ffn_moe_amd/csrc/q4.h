@@ -1,0 +1,80 @@
+// 4-bit expert weights with group scales: storage arithmetic, operand
+// conversion and the internal launchers (storage and semantics: moe_q4.h).
+#pragma once
+
+#include "moe_common.h"
+
+namespace moe {
+
+constexpr int kQ4Int = 0, kQ4E2m1 = 1;
+constexpr int kQ4TileK = 128;       // columns of a 1 KB code tile (16 rows)
+constexpr int kQ4TileBytes = 1024;
+
+struct Q4 {
+  int format, group;
+  int kb(int K) const { return (K + kQ4TileK - 1) / kQ4TileK; }             // code tiles along K
+  int stride(int K) const { return (kb(K) + 3) / 4 * 4 * (kQ4TileK / group); }  // scales per row
+};
+
+// One 32-bit word of codes as 8 bf16 operands.  INT4 yields 128 + code: the
+// four bits dropped into the mantissa of bf16 128 (one ulp is 1 there), two
+// codes per and-or; the 136 too much is taken off per group by the caller.
+// E2M1 converts on the gfx950 instruction, two codes at a time.
+template <int FMT>
+__device__ __forceinline__ bf16x8 q4_operand(uint32_t w) {
+  uint4 r;
+  if constexpr (FMT == kQ4Int) {
+    r.x = (w & 0x000f000fu) | 0x43004300u;
+    r.y = ((w >> 4) & 0x000f000fu) | 0x43004300u;
+    r.z = ((w >> 8) & 0x000f000fu) | 0x43004300u;
+    r.w = ((w >> 12) & 0x000f000fu) | 0x43004300u;
+  } else {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
+  }
+  return __builtin_bit_cast(bf16x8, r);
+}
+
+// Element i of an operand as the fp32 value of its code (exact).
+template <int FMT>
+__device__ __forceinline__ float q4_value(const bf16x8& b, int i) {
+  const float v = (float)b[i];
+  return FMT == kQ4Int ? v - 136.0f : v;
+}
+
+// The GPB scales of one row's code tile, as fp32.
+template <int GPB>
+__device__ __forceinline__ void q4_load_scales(const uint16_t* p, float (&s)[GPB]) {
+  if constexpr (GPB == 1) {
+    s[0] = bf16_bits_to_float(*p);
+  } else if constexpr (GPB == 2) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    s[0] = __uint_as_float(v << 16);
+    s[1] = __uint_as_float(v & 0xffff0000u);
+  } else {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    s[0] = __uint_as_float(v.x << 16);
+    s[1] = __uint_as_float(v.x & 0xffff0000u);
+    s[2] = __uint_as_float(v.y << 16);
+    s[3] = __uint_as_float(v.y & 0xffff0000u);
+  }
+}
+template <int GPB>
+__device__ __forceinline__ void q4_load_scales(const float* p, float (&s)[GPB]) {
+#pragma unroll
+  for (int i = 0; i < GPB; ++i) s[i] = p[i];
+}
+
+// Grouped products over any number of rows per expert (q4_w13.hip, q4_down.hip).
+hipError_t launch_q4_w13(const Shape& s, const Q4& q, const void* x, const int32_t* perm, const int32_t* offsets,
+                         const void* codes, const void* scales, void* h, hipStream_t st);
+hipError_t launch_q4_down(const Shape& s, const Q4& q, const void* h, const int32_t* offsets, const void* codes,
+                          const void* scales, void* y, hipStream_t st);
+
+// Quantisation of a stack of matrices [N, K] (q4_quantize.hip); gate_up: w1's row order.
+hipError_t launch_q4_quantize(const Q4& q, bool bf16, const void* w, long long matrices, int N, int K, bool gate_up,
+                              void* codes, void* scales, hipStream_t st);
+
+}  // namespace moe

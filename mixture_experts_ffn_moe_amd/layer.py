@@ -4,7 +4,7 @@ from __future__ import annotations
 
 import torch
 
-from ._lib import (MOE_BF16, moe_forward, moe_forward_shared, moe_get_shared_workspace_layout,
+from ._lib import (MOE_BF16, moe_forward, moe_forward_q4, moe_forward_shared, moe_get_shared_workspace_layout,
                    moe_get_workspace_layout, moe_shared_workspace_size, moe_workspace_size, y_nbytes)
 
 
@@ -55,6 +55,12 @@ class MoELayerBuffers:
 
     def forward(self, x, wg, bias, w1, w2, stream=None) -> torch.Tensor:
         moe_forward(self.shape, x, wg, bias, w1, w2, self.out, self.workspace, stream)
+        return self.out
+
+    def forward_q4(self, q4, x, wg, bias, w1_codes, w1_scales, w2_codes, w2_scales, stream=None) -> torch.Tensor:
+        """The layer over 4-bit expert weights (make_q4, moe_q4_quantize_w13, moe_q4_quantize_down)."""
+        moe_forward_q4(self.shape, q4, x, wg, bias, w1_codes, w1_scales, w2_codes, w2_scales, self.out,
+                       self.workspace, stream)
         return self.out
 
     def forward_shared(self, x, wg, bias, w1, w2, w1s, w2s, stream=None) -> torch.Tensor:

@@ -73,6 +73,13 @@ hipError_t launch_q4_w13(const Shape& s, const Q4& q, const void* x, const int32
 hipError_t launch_q4_down(const Shape& s, const Q4& q, const void* h, const int32_t* offsets, const void* codes,
                           const void* scales, void* y, hipStream_t st);
 
+// Small-token path of the whole layer (q4_decode.hip).
+bool q4_decode_supported(const Shape& s);
+hipError_t launch_q4_decode(const Shape& s, const Q4& q, const void* x, const float* wg, const float* bias,
+                            const void* w1c, const void* w1s, const void* w2c, const void* w2s, void* out,
+                            float* logits, int32_t* ids, float* w, int32_t* counts, int32_t* offsets, int32_t* perm,
+                            int32_t* inv, void* h, void* scratch, hipStream_t st);
+
 // Quantisation of a stack of matrices [N, K] (q4_quantize.hip); gate_up: w1's row order.
 hipError_t launch_q4_quantize(const Q4& q, bool bf16, const void* w, long long matrices, int N, int K, bool gate_up,
                               void* codes, void* scales, hipStream_t st);

@@ -114,8 +114,11 @@ moe_status moe_forward_q4(const moe_shape* shape, const moe_q4_spec* q4, const v
   int32_t* inv = (int32_t*)(ws + L.inv);
   void* h = ws + L.h;
   void* y = ws + L.y;
-  int32_t* hist = (int32_t*)(ws + L.scratch);
   hipStream_t st = (hipStream_t)stream;
+  if (moe::q4_decode_supported(s))
+    return hip_status(moe::launch_q4_decode(s, q, x, wg, bias, w1_codes, w1_scales, w2_codes, w2_scales, out, logits,
+                                            ids, w, counts, offsets, perm, inv, h, ws + L.scratch, st));
+  int32_t* hist = (int32_t*)(ws + L.scratch);
   MOE_CHECK(hip_status(moe::launch_route(s, x, wg, bias, logits, ids, w, st, hist)));
   MOE_CHECK(hip_status(moe::launch_permute_hist(s, ids, hist, counts, offsets, perm, inv, st)));
   MOE_CHECK(hip_status(moe::launch_q4_w13(s, q, x, perm, offsets, w1_codes, w1_scales, h, st)));

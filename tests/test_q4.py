@@ -147,6 +147,104 @@ def test_narrow_steps(m, dev, shape, fmt):
     run_steps(m, shape[:-1], fmt, shape[-1], seed=shape[0])
 
 
+# the small-token path: one unit per wave and fewer, more, cut ones; K tails of the down product; every token on
+# every expert; all tokens on the same experts
+DECODE = [(1, 2048, 64, 8, 128, 1), (1, 2048, 1, 1, 128, 1), (3, 4096, 16, 4, 128, 2), (8, 2048, 64, 8, 256, 1),
+          (16, 2048, 6, 6, 128, 2), (16, 4096, 64, 2, 128, 1), (5, 2048, 40, 8, 384, 1), (16, 2048, 16, 16, 128, 1)]
+
+
+@gpu
+@pytest.mark.parametrize("fmt,group", FORMATS)
+@pytest.mark.parametrize("shape", DECODE, ids=lambda s: "x".join(map(str, s)))
+def test_decode(m, dev, shape, fmt, group):
+    print(f"q4 decode {shape} {fmt} g{group}", flush=True)
+    c = Case(m, *shape, "bf16", fmt, group, seed=shape[0] + group, renorm=group != 64, bias=4.0 if shape[0] == 5 else None)
+    r = c.dense_steps(m)
+    out, dout = check_steps(c, r)
+    got, buf = c.forward(m)
+    v = buf.views()
+    for n in ("logits", "ids", "w", "counts", "offsets", "perm", "inv"):
+        assert torch.equal(v[n], r[n]), n
+    got = to_host_f32(got)
+    assert (np.abs(got - out) <= 2 * dout + 1e-30).all(), float(np.abs(got - out).max())
+    again, _ = c.forward(m)
+    assert np.array_equal(to_host_f32(again), got)
+
+
+@gpu
+@pytest.mark.parametrize("shape", [(2, 2048, 8, 3, 32, 2), (7, 2048, 24, 5, 96, 1), (16, 2048, 5, 2, 224, 1)])
+@pytest.mark.parametrize("fmt", ["int4", "e2m1"])
+def test_decode_narrow(m, dev, shape, fmt):
+    """Intermediate widths that end inside a 128-column tile on the small-token path."""
+    print(f"q4 decode {shape} {fmt}", flush=True)
+    c = Case(m, *shape, "bf16", fmt, 32, seed=shape[0])
+    out, dout = check_steps(c, c.dense_steps(m))
+    got = to_host_f32(c.forward(m)[0])
+    assert (np.abs(got - out) <= 2 * dout + 1e-30).all()
+
+
+@gpu
+def test_graph_replay_and_streams(m, dev):
+    """Captured and replayed with new tokens in the same buffers, eager calls between; another stream; both paths."""
+    for T in (6, 30):
+        c = Case(m, T, 2048, 12, 3, 128, 1, "bf16", "int4", 128, seed=T)
+        d = c.d
+        graphed, eager = m.MoELayerBuffers(c.shape), m.MoELayerBuffers(c.shape)
+        eager.forward_q4(c.q4, d["x"], d["wg"], d["bias"], *d["w"])
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            graphed.forward_q4(c.q4, d["x"], d["wg"], d["bias"], *d["w"])
+        for i in range(4):
+            d["x"].copy_(torch.randn(T, 2048, generator=torch.Generator().manual_seed(i)))
+            graphed.out.fill_(float("nan"))
+            graph.replay()
+            eager.forward_q4(c.q4, d["x"], d["wg"], d["bias"], *d["w"])
+            torch.cuda.synchronize()
+            assert torch.equal(graphed.out, eager.out), (T, i)
+        st = torch.cuda.Stream()
+        eager.out.fill_(float("nan"))
+        torch.cuda.synchronize()
+        eager.forward_q4(c.q4, d["x"], d["wg"], d["bias"], *d["w"], stream=st)
+        torch.cuda.synchronize()
+        assert torch.equal(graphed.out, eager.out)
+
+
+@gpu
+def test_quantized_layer_near_the_dense_one(m, dev):
+    """Quantise a dense bf16 layer and run both: the 4-bit layer equals the dense layer on the dequantised weights
+    (rounded to bf16, 2^-8 of each weight)."""
+    T, H, E, k, Im, mu = 24, 256, 6, 2, 128, 2
+    g = torch.Generator().manual_seed(2)
+    r = lambda *sh: torch.randn(*sh, generator=g)  # noqa: E731
+    x, wg = r(T, H).bfloat16().to(dev), (r(E, H) * 0.1).to(dev)
+    w1, w2 = (r(mu, E, 2 * Im, H) * 0.05).bfloat16().to(dev), (r(mu, E, H, Im) * 0.05).bfloat16().to(dev)
+    s, q4 = m.make_shape(T, H, E, k, Im, mu, "bf16"), m.make_q4("e2m1", 32)
+    z = m.moe_q4_get_sizes(s, q4)
+    st = {n: torch.empty(b, dtype=torch.uint8, device=dev) for n, b in z.items()}
+    m.moe_q4_quantize_w13(s, q4, w1, st["w1_codes"], st["w1_scales"])
+    m.moe_q4_quantize_down(s, q4, w2, st["w2_codes"], st["w2_scales"])
+    buf = m.MoELayerBuffers(s)
+    got = buf.forward_q4(q4, x, wg, None, st["w1_codes"], st["w1_scales"], st["w2_codes"], st["w2_scales"]).float().clone()
+
+    def dequantised(codes, scales, N, K, gate_up):
+        KB, S = -(-K // 128), qp.stride(K, 32)
+        b = codes.cpu().numpy().reshape(mu * E, N // 16, KB, 4, 16, 4, 4)
+        nib = np.stack([b & 15, b >> 4], -1).reshape(mu * E, N // 16, KB, 4, 16, 4, 8)   # lane / 16, lane % 16, word, nibble
+        c = nib.transpose(0, 1, 4, 2, 5, 3, 6).reshape(mu * E, N, KB * 128)[:, :, :K]
+        sc = scales.view(torch.bfloat16).float().cpu().numpy().reshape(mu * E, N, S)[:, :, :K // 32]
+        w = np.empty((mu * E, N, K))
+        w[:, qp.tile_rows(N, gate_up)] = qp.values(c, sc, "e2m1", 32)
+        return torch.from_numpy(w.astype(np.float32)).bfloat16().to(dev)
+
+    d1 = dequantised(st["w1_codes"], st["w1_scales"], 2 * Im, H, True).view(mu, E, 2 * Im, H)
+    d2 = dequantised(st["w2_codes"], st["w2_scales"], H, Im, False).view(mu, E, H, Im)
+    assert (d1.float() - w1.float()).norm() < 0.15 * w1.float().norm()  # 4 bits: a step of at most 1/3 of a value
+    ref = m.MoELayerBuffers(s).forward(x, wg, None, d1, d2).float()
+    # six roundings to bf16 apart (weights twice, h twice, out twice): 2^-8 each of independent terms
+    assert (got - ref).norm() <= 6 * 2.0 ** -8 * ref.norm()
+
+
 @gpu
 @pytest.mark.parametrize("fmt,group", [("int4", 32), ("int4", 128), ("e2m1", 64)])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])

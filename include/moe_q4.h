@@ -93,9 +93,10 @@ moe_status moe_q4_down(const moe_shape* shape, const moe_q4_spec* q4, const void
 
 /* moe_forward over 4-bit weights, in a workspace of moe_workspace_size(shape)
  * bytes with the same layout.  The small-token regime (bf16, T <= 16,
- * H % 2048 == 0, T * H <= 65536) takes a path of its own, as in moe_forward: routing is the same
- * bits as the step-wise path, the output matches it within rounding (sums in
- * another order, y never stored). */
+ * H % 2048 == 0, T rounded up to 4 times H and T times mu times Im rounded up
+ * to 128 both <= 65536) takes a path of its own, as in moe_forward: routing is
+ * the same bits as the step-wise path, the output matches it within rounding
+ * (sums in another order, y never stored). */
 moe_status moe_forward_q4(const moe_shape* shape, const moe_q4_spec* q4, const void* x,
                           const float* wg, const float* bias, const void* w1_codes,
                           const void* w1_scales, const void* w2_codes, const void* w2_scales,

@@ -172,7 +172,7 @@ __global__ __launch_bounds__(kW13Waves * 64) void decode_w13(
   __shared__ __attribute__((aligned(1024))) char buf[kW13Waves][kSlot];
   __shared__ RouteLds rs;
   route_finish(partial, bias, T, E, k, renorm != 0, blockIdx.x == 0, logits, ids, topw, counts, offsets_out, perm_out,
-               inv, active_out, rs);
+               inv, active_out, rs, [] {});
   const int* active = rs.act;
   const int* offsets = rs.off;
   const int* perm = rs.perm;

@@ -44,11 +44,15 @@ struct RouteLds {
   int perm[kDecT * kMaxK];       // permuted row -> route
 };
 
+//
+// `meanwhile` runs once the partials are summed and before the first barrier:
+// work of the caller whose own loads were issued before the call.
+template <typename F>
 __device__ __forceinline__ void route_finish(
     const double* __restrict__ partial, const float* __restrict__ bias, int T, int E, int k, bool renorm,
     bool out, float* __restrict__ logits, int32_t* __restrict__ ids, float* __restrict__ topw,
     int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ perm,
-    int32_t* __restrict__ inv, int32_t* __restrict__ active, RouteLds& S) {
+    int32_t* __restrict__ inv, int32_t* __restrict__ active, RouteLds& S, F meanwhile) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
 
   {  // logits: thread (r, e), partials summed in split order (rows past T
@@ -62,6 +66,7 @@ __device__ __forceinline__ void route_finish(
     S.lg[r][e] = L;
     if (out && r < T && e < E) logits[(size_t)r * E + e] = L;
   }
+  meanwhile();
   __syncthreads();
 
   {  // top-k and weights: wave = token, lane = expert (same rules as route.hip)

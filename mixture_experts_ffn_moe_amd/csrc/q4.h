@@ -20,14 +20,24 @@ struct Q4 {
 // four bits dropped into the mantissa of bf16 128 (one ulp is 1 there), two
 // codes per and-or; the 136 too much is taken off per group by the caller.
 // E2M1 converts on the gfx950 instruction, two codes at a time.
+struct Q4Consts {
+  // the and-or instruction takes one scalar and no literal: the mask is kept
+  // in a scalar register, the exponent bits in a vector register (as literals
+  // they cost an and and an or)
+  uint32_t mask, base;
+  __device__ __forceinline__ Q4Consts() {
+    asm("s_mov_b32 %0, 0xf000f" : "=s"(mask));
+    asm("v_mov_b32 %0, 0x43004300" : "=v"(base));
+  }
+};
 template <int FMT>
-__device__ __forceinline__ bf16x8 q4_operand(uint32_t w) {
+__device__ __forceinline__ bf16x8 q4_operand(uint32_t w, const Q4Consts& k) {
   uint4 r;
   if constexpr (FMT == kQ4Int) {
-    r.x = (w & 0x000f000fu) | 0x43004300u;
-    r.y = ((w >> 4) & 0x000f000fu) | 0x43004300u;
-    r.z = ((w >> 8) & 0x000f000fu) | 0x43004300u;
-    r.w = ((w >> 12) & 0x000f000fu) | 0x43004300u;
+    r.x = (w & k.mask) | k.base;
+    r.y = ((w >> 4) & k.mask) | k.base;
+    r.z = ((w >> 8) & k.mask) | k.base;
+    r.w = ((w >> 12) & k.mask) | k.base;
   } else {
     r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
     r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));

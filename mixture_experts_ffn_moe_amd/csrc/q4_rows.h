@@ -127,6 +127,7 @@ __global__ __launch_bounds__(kQrWaves * 64) void q4_rows(Q4Rows a) {
     sum_at[i] = (kbl[i] * GPB + c / (kChunks / GPB)) * MR + r;
   }
 
+  const Q4Consts kc;
   uint4 av[kLoads], cw[KC][NT], cn[KC][NT];
   float sw[KC][NT][GPB], sn[KC][NT][GPB];
   auto load_rows = [&](int b0) {
@@ -134,10 +135,10 @@ __global__ __launch_bounds__(kQrWaves * 64) void q4_rows(Q4Rows a) {
     for (int i = 0; i < kLoads; ++i) {
       const int b = b0 + kbl[i];
       const int seg = W13 ? 0 : b / a.KB;
-      const int kc = (b - seg * a.KB) * kQ4TileK + col[i];  // column within the matrix
-      const bool ok = row_ok[i] && b < nb && kc < a.K;
+      const int col0 = (b - seg * a.KB) * kQ4TileK + col[i];  // column within the matrix
+      const bool ok = row_ok[i] && b < nb && col0 < a.K;
       // a chunk that is not ok loads the row's first columns and is dropped
-      const uint4 v = *reinterpret_cast<const uint4*>(src[i] + (ok ? (size_t)seg * a.K + kc : 0));
+      const uint4 v = *reinterpret_cast<const uint4*>(src[i] + (ok ? (size_t)seg * a.K + col0 : 0));
       av[i] = ok ? v : make_uint4(0, 0, 0, 0);
     }
   };
@@ -206,7 +207,7 @@ __global__ __launch_bounds__(kQrWaves * 64) void q4_rows(Q4Rows a) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const uint32_t w = j == 0 ? cw[u][n].x : j == 1 ? cw[u][n].y : j == 2 ? cw[u][n].z : cw[u][n].w;
-              bv[n] = q4_operand<FMT>(w);
+              bv[n] = q4_operand<FMT>(w, kc);
             }
 #pragma unroll
             for (int m = 0; m < MT; ++m) {

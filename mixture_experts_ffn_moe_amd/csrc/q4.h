@@ -54,27 +54,30 @@ __device__ __forceinline__ float q4_value(const bf16x8& b, int i) {
   return FMT == kQ4Int ? v - 136.0f : v;
 }
 
-// The GPB scales of one row's code tile, as fp32.
-template <int GPB>
-__device__ __forceinline__ void q4_load_scales(const uint16_t* p, float (&s)[GPB]) {
-  if constexpr (GPB == 1) {
-    s[0] = bf16_bits_to_float(*p);
-  } else if constexpr (GPB == 2) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-    s[0] = __uint_as_float(v << 16);
-    s[1] = __uint_as_float(v & 0xffff0000u);
-  } else {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    s[0] = __uint_as_float(v.x << 16);
-    s[1] = __uint_as_float(v.x & 0xffff0000u);
-    s[2] = __uint_as_float(v.y << 16);
-    s[3] = __uint_as_float(v.y & 0xffff0000u);
-  }
+// Sum of v over the 4, 8 or 16 neighbouring lanes that hold one group (DPP: no
+// LDS round trip; mirrors do after the first two steps, whose sums are equal
+// in a quad).
+template <int CTRL>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
 }
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+  v = dpp_add<0xb1>(v);                           // quad_perm [1, 0, 3, 2]
+  v = dpp_add<0x4e>(v);                           // quad_perm [2, 3, 0, 1]
+  if constexpr (LANES >= 8) v = dpp_add<0x141>(v);   // row_half_mirror
+  if constexpr (LANES >= 16) v = dpp_add<0x140>(v);  // row_mirror
+  return v;
+}
+
+// Sum of 8 bf16 values, then over the lanes of one group (16 / GPB chunks of 8).
 template <int GPB>
-__device__ __forceinline__ void q4_load_scales(const float* p, float (&s)[GPB]) {
+__device__ __forceinline__ float q4_group_sum(const uint4& v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < GPB; ++i) s[i] = p[i];
+  for (int j = 0; j < 4; ++j) s += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
+  return lanes_sum<16 / GPB>(s);
 }
 
 // Grouped products over any number of rows per expert (q4_w13.hip, q4_down.hip).

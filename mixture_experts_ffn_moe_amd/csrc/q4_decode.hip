@@ -115,18 +115,6 @@ __device__ __forceinline__ void tile_mma(const uint4& c, const float (&s)[GPB], 
   pin(acc);
 }
 
-// Sum of 8 bf16 values, then over the lanes of one group (16 / GPB chunks of 8).
-template <int GPB>
-__device__ __forceinline__ float group_sum(const uint4& v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  float s = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) s += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
-#pragma unroll
-  for (int d = 1; d < 16 / GPB; d <<= 1) s += __shfl_xor(s, d);
-  return s;
-}
-
 // A barrier that orders LDS accesses and leaves loads in flight (the one of
 // __syncthreads waits for them).
 __device__ __forceinline__ void lds_barrier() {
@@ -168,7 +156,7 @@ __global__ __launch_bounds__(kDqWaves * 64) void q4_decode_w13(Q4DecodeArgs a) {
         const int t = q0 / (a.H / 8), c = q0 - t * (a.H / 8) + lane;
         *reinterpret_cast<uint4*>(xl + (t * (a.H / 8) + (c ^ t)) * 16) = xv[i];
         if constexpr (FMT == kQ4Int) {
-          const float sum = group_sum<GPB>(xv[i]);
+          const float sum = q4_group_sum<GPB>(xv[i]);
           if ((lane & (16 / GPB - 1)) == 0) xsum[c / (16 / GPB) * Tp + t] = -136.0f * sum;
         }
       }

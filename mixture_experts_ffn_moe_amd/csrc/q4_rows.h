@@ -1,22 +1,29 @@
 // Grouped products over 4-bit weights: one template for the gate|up product
 // with SwiGLU and for the down product.
 //
-// A workgroup of 8 waves takes up to 64 rows of one expert (16 MT, MT the
+// A workgroup of 8 waves takes up to 48 rows of one expert (16 MT, MT the
 // fewest 16-row tiles that hold them) and 256 weight rows, a wave 32 of them.
 // The codes are the bulk of the bytes and each is used once per row block, so
 // they go from HBM straight to registers in operand order (a wave loads whole
-// 1 KB tiles, 16 bytes a lane), `depth` steps ahead of their use.  The rows'
-// operands (x gathered through perm, or h) are shared by the waves: loaded
-// equally far ahead, they pass through LDS, double-buffered, one barrier a
-// step.  (Loads return in order: were the rows asked for later than the codes,
+// 1 KB tiles, 16 bytes a lane), four steps of 128 columns ahead of their use.
+// The rows' operands (x gathered through perm, or h) are shared by the waves
+// and go straight to LDS, as far ahead, in four slots, one barrier a step.
+// (Loads return in order: were the rows asked for later than the codes,
 // waiting for them would wait for every code in flight.)  A row of 256 bytes
-// (128 columns) keeps its 16-byte chunks XOR-swizzled by the row, so the 16
-// rows of a fragment read hit 16 bank groups.
+// (128 columns) has its 16-byte chunks XOR-swizzled by the row on the way, so
+// the 16 rows of a fragment read hit 16 bank groups.
+//
+// A row's scales are neighbours along K, so one step needs a few bytes of every
+// row's own line.  Four steps' scales are therefore loaded at once, each of the
+// four lane groups taking one step's, and handed to the other groups by a lane
+// permutation.  (Loaded step by step they were fetched anew each time, more
+// lines than the L1 holds: 168 against 121 us for the gate|up product at 256
+// tokens, two micro-shards.)
 //
 // INT4 codes enter as 128 + code (q4.h).  The 136 * sum(x) too much of a
-// group is the same for every weight row, so the thread that stages a chunk
-// sums it (8 values, then over the group's lanes), and -136 times the sum
-// starts the group's accumulator: no extra matrix instruction.
+// group is the same for every weight row: each wave sums the chunks that it
+// copied itself (8 values, then over the group's lanes), and -136 times the
+// sum starts the group's accumulator: no extra matrix instruction.
 #pragma once
 
 #include "q4.h"
@@ -74,7 +81,7 @@ __device__ __forceinline__ RowBlock find_block(const int32_t* __restrict__ offse
 
 constexpr int kQrTiles = 2;         // weight row tiles of a wave
 constexpr int kQrColTiles = kQrWaves * kQrTiles;
-constexpr int kQrLds = 16384;       // bytes of one buffer of staged rows, at most
+constexpr int kQrLds = 65536;       // bytes of the staged rows' slots, at most
 
 // An LDS barrier that leaves loads in flight.
 __device__ __forceinline__ void q4_lds_barrier() {
@@ -88,43 +95,68 @@ __device__ __forceinline__ void q4_lds_barrier() {
 // without the wait states that this instruction needs.
 __device__ __forceinline__ void q4_pin(f32x4& v) { asm volatile("" : "+v"(v)); }
 
+// One direct-to-LDS load of 16 bytes a lane from a 64-bit address (rows whose
+// offsets pass 32 bits); otherwise as dma16.
+__device__ __forceinline__ void dma16_at(uint32_t lds, const void* p) {
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(lds), "v"(p) : "memory", "m0");
+#pragma clang diagnostic pop
+}
+
+// All but the N newest loads have arrived, LDS copies among them.
+template <int N>
+__device__ __forceinline__ void q4_arrived() {
+  __builtin_amdgcn_sched_barrier(0);
+  wait_vmcnt<N>();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 template <typename XT, int FMT, int GPB, int MT, bool W13>
 struct RowsBody {
   static constexpr bool kBf16 = sizeof(XT) == 2;
   static constexpr int NT = kQrTiles;
   static constexpr int MR = 16 * MT;
-  static constexpr int KC = MT == 1 ? 2 : 1;           // code tiles per step and weight row tile
-  static constexpr int D = !kBf16 ? 2 : MT <= 2 ? 4 : GPB < 4 ? 3 : 2;  // steps in flight (registers allow no more)
+  static constexpr int D = 4;                          // steps in flight, and of one set of scales
   static constexpr int kRowBytes = kQ4TileK * (int)sizeof(XT);
   static constexpr int kChunks = kRowBytes / 16;       // 16-byte chunks of a row's tile
-  static constexpr int kStage = KC * MR * kChunks;     // chunks of a step
-  static constexpr int kLoads = (kStage + kQrWaves * 64 - 1) / (kQrWaves * 64);
+  // copies of 64 chunks that each wave makes per step: 32 or 64 rows (rows past
+  // the block repeat its last)
+  static constexpr int kCopies = (MT <= 2 ? 32 : 64) * kChunks / 64 / kQrWaves;
+  static constexpr int kSlot = kCopies * kQrWaves * 1024;
+  static constexpr int kSumRows = MT <= 2 ? 32 : 64;
   static constexpr bool kSums = kBf16 && FMT == kQ4Int;
   static constexpr int JG = 4 / GPB;                   // 32-column pieces per group
-  static constexpr int SW = kBf16 ? (GPB + 1) / 2 : GPB;  // words of a tile's scales
-  static_assert(kStage * 16 <= kQrLds, "a step fits its buffer");
+  static constexpr int kScaleBytes = GPB * (int)sizeof(XT);
+  static constexpr int SW = (kScaleBytes + 3) / 4;     // words of a tile's scales
+  static_assert(D * kSlot <= kQrLds, "the slots fit");
 
   const Q4Rows& a;
   const RowBlock& blk;
-  char* abuf;     // two buffers of kQrLds bytes
-  float* xsum;    // two of KC * GPB * MR
-  const int tid, lane, wave, fr, g, nb, tile0;
+  char* abuf;
+  float* xsum;    // [slot][group][row]
+  const int tid, lane, wave, fr, g, tile0;
+  int lseg = 0, lkb = 0;    // the step to load next (columns past the matrix's last tile: empty steps)
+  int KBp;                  // steps of a segment, a multiple of D
   const Q4Consts kc;
 
+  // Addresses are a uniform base (scalar registers) plus a 32-bit offset of the lane.
   const uint8_t* codes[NT];
   const XT* scales[NT];
   size_t seg_codes, seg_scales;
-  const XT* src[kLoads];
-  bool row_ok[kLoads];
-  uint4 av[D][kLoads];
-  uint4 cw[D][KC][NT];
-  uint32_t sw[D][KC][NT][SW];
+  uint32_t code_off, scale_off;
+  size_t src[kCopies];      // byte offset of the row a copy's lane reads
+  int col[kCopies];         // and its column within the tile
+  uint4 cw[D][NT];
+  uint32_t snext[NT][SW];   // scales of the next D steps, step lane / 16 of them in each lane
   f32x4 acc[MT][NT];
 
   __device__ __forceinline__ RowsBody(const Q4Rows& a_, const RowBlock& b_, int col_wg, char* abuf_, float* xsum_)
       : a(a_), blk(b_), abuf(abuf_), xsum(xsum_), tid(threadIdx.x), lane(threadIdx.x & 63),
         wave(__builtin_amdgcn_readfirstlane(threadIdx.x >> 6)), fr(threadIdx.x & 15), g((threadIdx.x & 63) >> 4),
-        nb(a_.segments * a_.KB), tile0((col_wg * kQrWaves + wave) * NT) {
+        tile0((col_wg * kQrWaves + wave) * NT) {
     // this wave's output tiles; past the last they repeat it and store nothing
     seg_codes = (size_t)a.E * (a.N / 16) * a.KB * kQ4TileBytes;
     seg_scales = (size_t)a.E * a.N * a.S;
@@ -134,15 +166,20 @@ struct RowsBody {
       const int ct = min(tile0 + n, a.tiles - 1);
       const int m = W13 ? ct / per : 0, it = W13 ? ct % per : ct;
       const size_t tile = ((size_t)m * a.E + blk.e) * per + it;
-      codes[n] = a.codes + tile * a.KB * kQ4TileBytes + lane * 16;
-      scales[n] = (const XT*)a.scales + (tile * 16 + fr) * a.S;
+      codes[n] = a.codes + tile * a.KB * kQ4TileBytes;
+      scales[n] = (const XT*)a.scales + tile * 16 * a.S;
     }
+    code_off = lane * 16;
+    scale_off = (uint32_t)((fr * a.S + g * GPB) * (int)sizeof(XT));
+    KBp = (a.KB + D - 1) / D * D;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int p = blk.row0 + chunk_row(i);
-      row_ok[i] = p < blk.end && in_stage(i);
-      const int pc = min(p, blk.end - 1);
-      src[i] = (const XT*)a.x + (size_t)(W13 ? a.perm[pc] / a.k : pc) * a.ldx;
+    for (int i = 0; i < kCopies; ++i) {
+      // chunk q of the slot holds chunk (q % kChunks) ^ swizzle of row q / kChunks
+      const int q = (i * kQrWaves + wave) * 64 + lane, r = q / kChunks;
+      const int c = (q % kChunks) ^ (kBf16 ? (r & 15) : (r & 15) << 1);
+      const int p = min(blk.row0 + r, blk.end - 1);
+      src[i] = (size_t)(W13 ? a.perm[p] / a.k : p) * a.ldx * sizeof(XT);
+      col[i] = c * (16 / (int)sizeof(XT));
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -150,65 +187,61 @@ struct RowsBody {
       for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
-  // chunk i of this thread within a step: tile of the step, row, chunk of the row
-  __device__ __forceinline__ int chunk_index(int i) const { return tid + i * kQrWaves * 64; }
-  __device__ __forceinline__ bool in_stage(int i) const { return chunk_index(i) < kStage; }
-  __device__ __forceinline__ int chunk_col(int i) const { return chunk_index(i) % kChunks; }
-  __device__ __forceinline__ int chunk_row(int i) const { return chunk_index(i) / kChunks % MR; }
-  __device__ __forceinline__ int chunk_tile(int i) const { return chunk_index(i) / (kChunks * MR); }
-
-  __device__ __forceinline__ void load_rows(int b0, uint4 (&v)[kLoads]) const {
+  // A step is 128 columns, tile kb of segment seg: its rows to the slot, its
+  // codes to registers, and on to the step after it.  An empty step loads the
+  // segment's last tile again.
+  __device__ __forceinline__ void next(int slot, uint4 (&c)[NT]) {
+    const int kb = min(lkb, a.KB - 1), seg = W13 ? 0 : lseg, k0 = kb * kQ4TileK;
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int b = b0 + chunk_tile(i);
-      const int seg = W13 ? 0 : b / a.KB;
-      const int col0 = (b - seg * a.KB) * kQ4TileK + chunk_col(i) * (16 / (int)sizeof(XT));  // within the matrix
-      const bool ok = row_ok[i] && b < nb && col0 < a.K;
-      // a chunk that is not ok loads the row's first columns; it is dropped when it is stored
-      v[i] = *reinterpret_cast<const uint4*>(src[i] + (ok ? (size_t)seg * a.K + col0 : 0));
+    for (int i = 0; i < kCopies; ++i) {
+      // columns past the matrix meet codes and scales of zero: the row's first columns will do
+      const int k = seg * a.K + (k0 + col[i] < a.K ? k0 + col[i] : 0);
+      const uint32_t lds = (uint32_t)(uintptr_t)abuf + (uint32_t)(slot * kSlot + (i * kQrWaves + wave) * 1024);
+      if constexpr (kBf16)  // fewer than 2^31 elements: offsets below 4 GB
+        dma16(lds, a.x, (uint32_t)src[i] + (uint32_t)k * 2u);
+      else
+        dma16_at(lds, (const char*)a.x + src[i] + (size_t)k * 4);
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      c[n] = *reinterpret_cast<const uint4*>(codes[n] + seg * seg_codes + (size_t)kb * kQ4TileBytes + code_off);
+    const bool wrap = lkb + 1 == KBp;
+    lkb = wrap ? 0 : lkb + 1;
+    lseg = wrap ? lseg + 1 : lseg;
   }
-  __device__ __forceinline__ void load_codes(int b0, uint4 (&c)[KC][NT], uint32_t (&s)[KC][NT][SW]) const {
+  // The scales of the D steps from the next one on.
+  __device__ __forceinline__ void next_scales() {
+    const int seg = W13 ? 0 : lseg;
 #pragma unroll
-    for (int u = 0; u < KC; ++u) {
-      const int b = min(b0 + u, nb - 1);  // past the end: loaded again, not used
-      const int seg = W13 ? 0 : b / a.KB;
-      const int kb = b - seg * a.KB;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        c[u][n] = *reinterpret_cast<const uint4*>(codes[n] + seg * seg_codes + (size_t)kb * kQ4TileBytes);
-        const XT* p = scales[n] + seg * seg_scales + kb * GPB;
-        if constexpr (!kBf16) {
-#pragma unroll
-          for (int q = 0; q < GPB; ++q) s[u][n][q] = __float_as_uint(p[q]);
-        } else if constexpr (GPB == 1) {
-          s[u][n][0] = *p;
-        } else {
-#pragma unroll
-          for (int q = 0; q < SW; ++q) s[u][n][q] = reinterpret_cast<const uint32_t*>(p)[q];
-        }
+    for (int n = 0; n < NT; ++n) {
+      const char* p = (const char*)(scales[n] + seg * seg_scales + lkb * GPB) + scale_off;
+      if constexpr (kScaleBytes == 2) {
+        snext[n][0] = *reinterpret_cast<const uint16_t*>(p);
+      } else if constexpr (kScaleBytes == 4) {
+        snext[n][0] = *reinterpret_cast<const uint32_t*>(p);
+      } else if constexpr (kScaleBytes == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        snext[n][0] = v.x;
+        snext[n][1] = v.y;
+      } else {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        snext[n][0] = v.x;
+        snext[n][1] = v.y;
+        snext[n][2] = v.z;
+        snext[n][3] = v.w;
       }
     }
   }
-  __device__ __forceinline__ void store_rows(int b0, const uint4 (&v)[kLoads], int buf) const {
+  // Sums of the chunks this wave copied to the slot (they have arrived).
+  __device__ __forceinline__ void sum_rows(int slot) const {
+    if constexpr (kSums) {
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i) {
-      const int u = chunk_tile(i), r = chunk_row(i), c = chunk_col(i), b = b0 + u;
-      const int kb = W13 ? b : b % a.KB;
-      const bool ok = row_ok[i] && b < nb && kb * kQ4TileK + c * (16 / (int)sizeof(XT)) < a.K;
-      const uint4 w = ok ? v[i] : make_uint4(0, 0, 0, 0);
-      const int x = kBf16 ? (r & 15) : (r & 15) << 1;
-      if (in_stage(i))
-        *reinterpret_cast<uint4*>(abuf + buf * kQrLds + (u * MR + r) * kRowBytes + ((c ^ x) * 16)) = w;
-      if constexpr (kSums) {
-        const uint32_t q[4] = {w.x, w.y, w.z, w.w};
-        float s = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s += __uint_as_float(q[j] << 16) + __uint_as_float(q[j] & 0xffff0000u);
-#pragma unroll
-        for (int d = 1; d < kChunks / GPB; d <<= 1) s += __shfl_xor(s, d);
-        if ((tid & (kChunks / GPB - 1)) == 0 && in_stage(i))
-          xsum[buf * (KC * GPB * MR) + (u * GPB + c / (kChunks / GPB)) * MR + r] = -136.0f * s;
+      for (int i = 0; i < kCopies; ++i) {
+        const int q = (i * kQrWaves + wave) * 64 + lane, r = q / kChunks;
+        // the xor swizzle permutes a row's groups and the chunks within one
+        const float s = q4_group_sum<GPB>(*reinterpret_cast<const uint4*>(abuf + slot * kSlot + q * 16));
+        const int c = (lane & 15) ^ (r & 15);
+        if ((lane & (16 / GPB - 1)) == 0) xsum[(slot * GPB + c / (16 / GPB)) * kSumRows + r] = -136.0f * s;
       }
     }
   }
@@ -216,58 +249,55 @@ struct RowsBody {
     if constexpr (!kBf16) return __uint_as_float(s[q]);
     return __uint_as_float((q & 1) ? s[q / 2] & 0xffff0000u : s[q / 2] << 16);
   }
-  __device__ __forceinline__ void products(int b0, const uint4 (&c)[KC][NT], const uint32_t (&s)[KC][NT][SW], int buf) {
+  __device__ __forceinline__ void products(const uint4 (&c)[NT], const uint32_t (&s)[NT][SW], int slot) {
+    const char* rows = abuf + slot * kSlot + fr * kRowBytes;
 #pragma unroll
-    for (int u = 0; u < KC; ++u) {
-      if (b0 + u < nb) {
+    for (int gr = 0; gr < GPB; ++gr) {
+      bf16x8 bv[JG][NT];
+      float f[NT];
 #pragma unroll
-        for (int gr = 0; gr < GPB; ++gr) {
-          f32x4 part[MT][NT];
+      for (int n = 0; n < NT; ++n) {
+        f[n] = scale(s[n], gr);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            f32x4 start = f32x4{0.f, 0.f, 0.f, 0.f};
-            if constexpr (kSums)
-              start = *reinterpret_cast<const f32x4*>(&xsum[buf * (KC * GPB * MR) + (u * GPB + gr) * MR + 16 * m + 4 * g]);
+        for (int jj = 0; jj < JG; ++jj) {
+          const int j = gr * JG + jj;
+          bv[jj][n] = q4_operand<FMT>(j == 0 ? c[n].x : j == 1 ? c[n].y : j == 2 ? c[n].z : c[n].w, kc);
+        }
+      }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) part[m][n] = start;
-          }
+      for (int m = 0; m < MT; ++m) {
+        const char* row = rows + 16 * m * kRowBytes;
+        f32x4 part[NT];
+        f32x4 start = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (kSums)
+          start = *reinterpret_cast<const f32x4*>(&xsum[(slot * GPB + gr) * kSumRows + 16 * m + 4 * g]);
 #pragma unroll
-          for (int j = gr * JG; j < (gr + 1) * JG; ++j) {
-            bf16x8 bv[NT];
+        for (int n = 0; n < NT; ++n) part[n] = start;
+#pragma unroll
+        for (int jj = 0; jj < JG; ++jj) {
+          const int j = gr * JG + jj;
+          if constexpr (kBf16) {
+            const bf16x8 av8 = *reinterpret_cast<const bf16x8*>(row + (((4 * j + g) ^ fr) * 16));
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-              bv[n] = q4_operand<FMT>(j == 0 ? c[u][n].x : j == 1 ? c[u][n].y : j == 2 ? c[u][n].z : c[u][n].w, kc);
+              part[n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av8, bv[jj][n], part[n], 0, 0, 0);
+          } else {
+            // fp32 operands: element i of the four lane groups is one k-step of 4
+            const int ch = 2 * (4 * j + g);
+            const f32x4 lo = *reinterpret_cast<const f32x4*>(row + ((ch ^ (fr << 1)) * 16));
+            const f32x4 hi = *reinterpret_cast<const f32x4*>(row + (((ch + 1) ^ (fr << 1)) * 16));
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const char* row = abuf + buf * kQrLds + (u * MR + 16 * m + fr) * kRowBytes;
-              if constexpr (kBf16) {
-                const bf16x8 av8 = *reinterpret_cast<const bf16x8*>(row + (((4 * j + g) ^ fr) * 16));
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
-                  part[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(av8, bv[n], part[m][n], 0, 0, 0);
-              } else {
-                // fp32 operands: element i of the four lane groups is one k-step of 4
-                const int ch = 2 * (4 * j + g);
-                const f32x4 lo = *reinterpret_cast<const f32x4*>(row + ((ch ^ (fr << 1)) * 16));
-                const f32x4 hi = *reinterpret_cast<const f32x4*>(row + (((ch + 1) ^ (fr << 1)) * 16));
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-#pragma unroll
-                  for (int n = 0; n < NT; ++n)
-                    part[m][n] = __builtin_amdgcn_mfma_f32_16x16x4f32(i < 4 ? lo[i] : hi[i - 4], q4_value<FMT>(bv[n], i),
-                                                                      part[m][n], 0, 0, 0);
-              }
-            }
+              for (int n = 0; n < NT; ++n)
+                part[n] = __builtin_amdgcn_mfma_f32_16x16x4f32(i < 4 ? lo[i] : hi[i - 4], q4_value<FMT>(bv[jj][n], i),
+                                                               part[n], 0, 0, 0);
           }
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const float f = scale(s[u][n], gr);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(f, part[m][n][r], acc[m][n][r]);
-            }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[m][n][r] = fmaf(f[n], part[n][r], acc[m][n][r]);
       }
     }
 #pragma unroll
@@ -276,54 +306,63 @@ struct RowsBody {
       for (int n = 0; n < NT; ++n) q4_pin(acc[m][n]);
   }
 
-  // Step k of the slot d = k mod D: its products, then the slot's codes and the
-  // next slot's rows (which go to LDS first) for D steps later.
+  // Step d of a set of D, in slot d: once the next step's rows are here, their
+  // sums beside this step's products; when every wave is done with the slot,
+  // the copies and loads of the step D later into it.  Behind the copies of the
+  // next step lie that step's codes and all of the D - 2 steps after it (and,
+  // not counted on, a set of scales).
   template <int d, bool kLoad>
-  __device__ __forceinline__ void step(int k) {
-    constexpr int e = (d + 1) % D;
-    products(k * KC, cw[d], sw[d], k & 1);
-    if (kLoad) load_codes((k + D) * KC, cw[d], sw[d]);
-    store_rows((k + 1) * KC, av[e], (k + 1) & 1);
-    if (kLoad) load_rows((k + 1 + D) * KC, av[e]);
-    __builtin_amdgcn_sched_barrier(0);
+  __device__ __forceinline__ void step(const uint32_t (&sset)[NT][SW], bool any) {
+    if constexpr (kLoad)
+      q4_arrived<NT + (D - 2) * (kCopies + NT)>();
+    else
+      q4_arrived<0>();
+    sum_rows((d + 1) % D);  // past the last step: of an old slot, not used
+    if (any) {
+      uint32_t s[NT][SW];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int w = 0; w < SW; ++w)
+          s[n][w] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * d + fr) * 4, (int)sset[n][w]);
+      products(cw[d], s, d);
+    }
     q4_lds_barrier();
+    if constexpr (kLoad) next(d, cw[d]);
+    __builtin_amdgcn_sched_barrier(0);
   }
-  template <int d>
-  __device__ __forceinline__ void round(int k) {  // D steps with their loads
-    if constexpr (d < D) {
-      step<d, true>(k + d);
-      round<d + 1>(k);
-    }
-  }
-  template <int d>
-  __device__ __forceinline__ void last(int k, int steps) {  // up to 2 D - 1 steps; loads only for those there are
-    if constexpr (d < 2 * D - 1) {
-      if (k + d >= steps) return;
-      if (k + d + D < steps)
-        step<d % D, true>(k + d);
-      else
-        step<d % D, false>(k + d);
-      last<d + 1>(k, steps);
-    }
-  }
-  template <int d>
-  __device__ __forceinline__ void fill() {
-    if constexpr (d < D) {
-      load_rows(d * KC, av[d]);
-      load_codes(d * KC, cw[d], sw[d]);
-      fill<d + 1>();
-    }
+  // D steps, the first at tile kb of its segment.
+  template <bool kLoad>
+  __device__ __forceinline__ void set(int kb) {
+    uint32_t scur[NT][SW];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int w = 0; w < SW; ++w) scur[n][w] = snext[n][w];
+    if constexpr (kLoad) next_scales();
+    step<0, kLoad>(scur, true);
+    step<1, kLoad>(scur, kb + 1 < a.KB);
+    step<2, kLoad>(scur, kb + 2 < a.KB);
+    step<3, kLoad>(scur, kb + 3 < a.KB);
   }
   __device__ __forceinline__ void sums() {
-    const int steps = (nb + KC - 1) / KC;
-    fill<0>();
-    __builtin_amdgcn_sched_barrier(0);
-    store_rows(0, av[0], 0);
-    load_rows(D * KC, av[0]);
+    static_assert(D == 4, "set() and the scales' lane groups");
+    next_scales();
+    next(0, cw[0]);
+    next(1, cw[1]);
+    next(2, cw[2]);
+    next(3, cw[3]);
+    q4_arrived<NT + (D - 1) * (kCopies + NT)>();
+    sum_rows(0);
     q4_lds_barrier();
-    int k = 0;
-    for (; k + 2 * D <= steps; k += D) round<0>(k);
-    last<0>(k, steps);
+    const int sets = a.segments * (KBp / D);
+    int kb = 0;
+    for (int i = 0; i + 1 < sets; ++i) {
+      set<true>(kb);
+      kb = kb + D == KBp ? 0 : kb + D;
+    }
+    set<false>(kb);
+    __syncthreads();  // the slots are used again; no copy is in flight
   }
 
   // D layout of the matrix instruction: register r of a lane holds row 4 (lane/16) + r, column lane%16
@@ -363,7 +402,7 @@ struct RowsBody {
       // block-scaled half y: the workgroup's columns are one block of 256
       // (repeated tiles past H repeat a stored column: the maximum is unchanged)
       static_assert(kQrColTiles * 16 == kYBlock, "one y block per workgroup");
-      float* rowmax = reinterpret_cast<float*>(abuf);  // [wave][row]; the last step's barrier has passed
+      float* rowmax = reinterpret_cast<float*>(abuf);  // [wave][row]
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
@@ -406,10 +445,10 @@ struct RowsBody {
 };
 
 template <typename XT, int FMT, int GPB, bool W13>
-__global__ __launch_bounds__(kQrWaves * 64) void q4_rows(Q4Rows a) {
-  constexpr int kMaxMT = sizeof(XT) == 2 ? 4 : 2;
-  __shared__ __attribute__((aligned(16))) char abuf[2 * kQrLds];
-  __shared__ __attribute__((aligned(16))) float xsum[2 * GPB * 16 * kMaxMT];
+__global__ __launch_bounds__(kQrWaves * 64, 4) void q4_rows(Q4Rows a) {  // two workgroups per CU
+  constexpr int kMaxMT = sizeof(XT) == 2 ? 3 : 2;
+  __shared__ __attribute__((aligned(1024))) char abuf[kQrLds];
+  __shared__ __attribute__((aligned(16))) float xsum[4 * GPB * 64];
   const int cols = (a.tiles + kQrColTiles - 1) / kQrColTiles;  // workgroups across the output
   const int col_wg = blockIdx.x % cols;
   const RowBlock blk = find_block<16 * kMaxMT>(a.offsets, a.E, blockIdx.x / cols);
@@ -420,10 +459,7 @@ __global__ __launch_bounds__(kQrWaves * 64) void q4_rows(Q4Rows a) {
   } else if (mt == 2) {
     RowsBody<XT, FMT, GPB, 2, W13>(a, blk, col_wg, abuf, xsum).run(col_wg);
   } else if constexpr (kMaxMT > 2) {
-    if (mt == 3)
-      RowsBody<XT, FMT, GPB, 3, W13>(a, blk, col_wg, abuf, xsum).run(col_wg);
-    else
-      RowsBody<XT, FMT, GPB, 4, W13>(a, blk, col_wg, abuf, xsum).run(col_wg);
+    RowsBody<XT, FMT, GPB, 3, W13>(a, blk, col_wg, abuf, xsum).run(col_wg);
   }
 }
 
@@ -431,7 +467,7 @@ __global__ __launch_bounds__(kQrWaves * 64) void q4_rows(Q4Rows a) {
 // host; workgroups past the last exit at once).
 template <typename XT, bool W13>
 inline hipError_t launch_rows_of(const Shape& s, const Q4& q, const Q4Rows& a, hipStream_t st) {
-  constexpr int kRows = sizeof(XT) == 2 ? 64 : 32;
+  constexpr int kRows = sizeof(XT) == 2 ? 48 : 32;
   const long long blocks = s.R() / kRows + (s.R() < s.E ? s.R() : s.E);
   const dim3 grid((unsigned)(blocks * ((a.tiles + kQrColTiles - 1) / kQrColTiles))), block(kQrWaves * 64);
 #define Q4_GO(FMT, GPB) hipLaunchKernelGGL((q4_rows<XT, FMT, GPB, W13>), grid, block, 0, st, a)

@@ -53,7 +53,8 @@ __device__ __forceinline__ void load8f(const uint16_t* p, float (&v)[8]) {
 }
 
 // ---------------------------------------------------------------------------
-// 1. router partials: block s covers hidden [s*H/kSplit, (s+1)*H/kSplit), its
+// 1. router partials of token tile blockIdx.y (one tile on the decode path):
+// block s covers hidden [s*H/kSplit, (s+1)*H/kSplit), its
 // wave w the quarter w % 4 of that for experts [16*(w/4), 16*(w/4) + 16);
 // partial[s][t][e] (fp64, the quarters summed in a fixed order).
 constexpr int kRouteWaves = 16;
@@ -65,6 +66,9 @@ __global__ __launch_bounds__(kRouteWaves * 64) void decode_route_partial(const u
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int tl = lane & 15, g = lane >> 4;
   const int hw = wave & 3, q = wave >> 2;  // hidden quarter, expert tile
+  x += (size_t)blockIdx.y * kDecT * H;
+  T = min(T - (int)blockIdx.y * kDecT, kDecT);
+  partial += (size_t)blockIdx.y * kSplit * kDecT * kMaxExperts;
   const int hs = H / kSplit, hq = hs / 4;
   const int hb = blockIdx.x * hs + hw * hq;
   // tokens past T and experts past E read the last valid row: their partials
@@ -107,6 +111,47 @@ __global__ __launch_bounds__(kRouteWaves * 64) void decode_route_partial(const u
     partial[((size_t)blockIdx.x * kDecT + r) * kMaxExperts + e] =
         ((part[0][r][e] + part[1][r][e]) + part[2][r][e]) + part[3][r][e];
   }
+}
+
+// Routing of more tokens from the same partials, one workgroup per tile of 16:
+// logits, top-k, weights, and the expert counts of the tile (as route_kernel
+// leaves them for the permutation).  A token is a wave, an expert a lane.
+__global__ __launch_bounds__(kRouteWaves * 64) void route_tiles_finish(
+    const double* __restrict__ partial, const float* __restrict__ bias, int T, int E, int k, int renorm,
+    float* __restrict__ logits, int32_t* __restrict__ ids, float* __restrict__ topw, int32_t* __restrict__ hist) {
+  __shared__ int hcnt[kMaxExperts];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int t = blockIdx.x * kDecT + wave;
+  if (tid < kMaxExperts) hcnt[tid] = 0;
+  __syncthreads();
+  if (t < T) {
+    const double* p = partial + (size_t)blockIdx.x * kSplit * kDecT * kMaxExperts + wave * kMaxExperts + lane;
+    double s = 0.0;
+#pragma unroll
+    for (int b = 0; b < kSplit; ++b) s += p[(size_t)b * kDecT * kMaxExperts];
+    const double bb = (bias != nullptr && lane < E) ? (double)bias[lane] : 0.0;
+    const float L = (float)(s + bb);
+    if (lane < E) logits[(size_t)t * E + lane] = L;
+    uint32_t key = lane < E ? orderable(L) : 0u;
+    float mine = 0.0f, first = 0.0f;
+    for (int j = 0; j < k; ++j) {
+      const uint32_t m = wave_max_u32(key);
+      const int win = __ffsll((long long)__ballot(key == m)) - 1;
+      const float Lw = from_orderable(m);
+      if (j == 0) first = Lw;
+      if (lane == j) mine = Lw;
+      if (lane == win) key = 0;
+      if (lane == 0) {
+        ids[(size_t)t * k + j] = win;
+        atomicAdd(&hcnt[win], 1);
+      }
+    }
+    const double ex = (lane < k) ? exp((double)mine - (double)first) : 0.0;
+    const double sum = wave_sum_f64(renorm ? ex : (lane < E ? exp((double)L - (double)first) : 0.0));
+    if (lane < k) topw[(size_t)t * k + lane] = (float)(ex / sum);
+  }
+  __syncthreads();
+  if (tid < kMaxExperts) hist[(size_t)blockIdx.x * kMaxExperts + tid] = hcnt[tid];
 }
 
 // ---------------------------------------------------------------------------
@@ -374,6 +419,19 @@ hipError_t launch_decode_route_partial(const Shape& s, const void* x, const floa
                                        hipStream_t st) {
   hipLaunchKernelGGL(decode_route_partial, dim3(kSplit), dim3(kRouteWaves * 64), 0, st, (const uint16_t*)x, wg,
                      s.T, s.H, s.E, partial);
+  return hipGetLastError();
+}
+
+size_t route_tiles_bytes(const Shape& s) { return (size_t)((s.T + kDecT - 1) / kDecT) * kRoutePartialBytes; }
+
+hipError_t launch_route_tiles(const Shape& s, const void* x, const float* wg, const float* bias, double* partial,
+                              float* logits, int32_t* ids, float* w, int32_t* hist, hipStream_t st) {
+  static_assert(kDecT == kRouteTokTile, "one histogram row per tile");
+  const int tiles = (s.T + kDecT - 1) / kDecT;
+  hipLaunchKernelGGL(decode_route_partial, dim3(kSplit, tiles), dim3(kRouteWaves * 64), 0, st, (const uint16_t*)x, wg,
+                     s.T, s.H, s.E, partial);
+  hipLaunchKernelGGL(route_tiles_finish, dim3(tiles), dim3(kRouteWaves * 64), 0, st, partial, bias, s.T, s.E, s.k,
+                     (int)s.renorm, logits, ids, w, hist);
   return hipGetLastError();
 }
 

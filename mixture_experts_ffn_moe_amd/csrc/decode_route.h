@@ -19,6 +19,13 @@ constexpr size_t kRoutePartialBytes = (size_t)kSplit * kDecT * kMaxExperts * siz
 hipError_t launch_decode_route_partial(const Shape& s, const void* x, const float* wg, double* partial,
                                        hipStream_t st);
 
+// Routing of any number of tokens from such partials, one set per tile of
+// kDecT tokens (route_tiles_bytes in all; bf16, H % (kSplit * 128) == 0):
+// launch_route's outputs, the logits summed in another order (decode.hip).
+size_t route_tiles_bytes(const Shape& s);
+hipError_t launch_route_tiles(const Shape& s, const void* x, const float* wg, const float* bias, double* partial,
+                              float* logits, int32_t* ids, float* w, int32_t* hist, hipStream_t st);
+
 namespace {
 
 __device__ __forceinline__ double wave_sum_f64(double v) {

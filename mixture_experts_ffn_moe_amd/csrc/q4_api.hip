@@ -2,6 +2,7 @@
 // launch sequence.
 #include "../../include/moe_q4.h"
 #include "api_check.h"
+#include "decode_route.h"
 #include "q4.h"
 
 using namespace moe_api;
@@ -26,6 +27,16 @@ void sizes_of(const Shape& s, const Q4& q, moe_q4_sizes* z) {
   z->w1_scales = mats * 2 * s.Im * q.stride(s.H) * e;
   z->w2_codes = mats * (s.H / 16) * q.kb(s.Im) * moe::kQ4TileBytes;
   z->w2_scales = mats * s.H * q.stride(s.Im) * e;
+}
+
+// The router with H split over 16 workgroups per 16 tokens, and a second launch
+// that adds the parts, instead of one workgroup per 16 tokens, which takes 44
+// us however few they are: 256 tokens 13 us, 1024 tokens 23 us; at 2048 the
+// two are even.
+constexpr int kSplitRouteTokens = 1024;
+bool split_route(const Shape& s) {
+  return s.bf16 && s.T <= kSplitRouteTokens && s.H % (moe::kSplit * 128) == 0 &&
+         moe::route_tiles_bytes(s) <= y_bytes(s, s.R());
 }
 
 }  // namespace
@@ -119,7 +130,10 @@ moe_status moe_forward_q4(const moe_shape* shape, const moe_q4_spec* q4, const v
     return hip_status(moe::launch_q4_decode(s, q, x, wg, bias, w1_codes, w1_scales, w2_codes, w2_scales, out, logits,
                                             ids, w, counts, offsets, perm, inv, h, ws + L.scratch, st));
   int32_t* hist = (int32_t*)(ws + L.scratch);
-  MOE_CHECK(hip_status(moe::launch_route(s, x, wg, bias, logits, ids, w, st, hist)));
+  if (split_route(s))  // the partial sums lie where y will
+    MOE_CHECK(hip_status(moe::launch_route_tiles(s, x, wg, bias, (double*)y, logits, ids, w, hist, st)));
+  else
+    MOE_CHECK(hip_status(moe::launch_route(s, x, wg, bias, logits, ids, w, st, hist)));
   MOE_CHECK(hip_status(moe::launch_permute_hist(s, ids, hist, counts, offsets, perm, inv, st)));
   MOE_CHECK(hip_status(moe::launch_q4_w13(s, q, x, perm, offsets, w1_codes, w1_scales, h, st)));
   MOE_CHECK(hip_status(moe::launch_q4_down(s, q, h, offsets, w2_codes, w2_scales, y, st)));

@@ -184,6 +184,21 @@ def test_decode_narrow(m, dev, shape, fmt):
 
 
 @gpu
+@pytest.mark.parametrize("T,H,E,k", [(17, 2048, 64, 8), (40, 4096, 5, 2), (257, 2048, 33, 3), (1024, 2048, 64, 4),
+                                     (1025, 2048, 8, 2), (30, 2048, 4, 1)])
+def test_routing_of_batches(m, dev, T, H, E, k):
+    """The one call's routing of medium batches: the step-wise path's bits."""
+    print(f"q4 routing T={T} H={H} E={E} k={k}", flush=True)
+    c = Case(m, T, H, E, k, 128, 1, "bf16", "int4", 128, seed=T, bias=2.0 if T == 40 else None, renorm=T != 257)
+    r = c.dense_steps(m)
+    got, buf = c.forward(m)
+    v = buf.views()
+    for n in ("logits", "ids", "w", "counts", "offsets", "perm", "inv", "h"):
+        assert torch.equal(v[n], r[n]), n
+    assert torch.equal(got, r["out"])
+
+
+@gpu
 def test_graph_replay_and_streams(m, dev):
     """Captured and replayed with new tokens in the same buffers, eager calls between; another stream; both paths."""
     for T in (6, 30):

@@ -347,7 +347,7 @@ __global__ __launch_bounds__(kFbThreads) void finalize_backward(const YT* __rest
 }
 
 // ---------------------------------------------------------------------------
-// Gradient of the router's weight on v_mfma_f32_16x16x4_f32: a lane supplies
+// Gradient of the router's weight, fp32 x, on v_mfma_f32_16x16x4_f32: a lane supplies
 // one token's (k = lane/16) d_logits of expert 16 mt + lane%16 as A and one
 // token's x column as B, so both operands are taken as they lie in memory.  A
 // lane loads four neighbouring columns 4 (lane%16) + q; column tile q then
@@ -365,17 +365,9 @@ inline int wgrad_splits(int T, int H) {
   return std::max(1, std::min(kWgBlocks / (H / kWgCols), (T + kWgMinTokens - 1) / kWgMinTokens));
 }
 
-__device__ __forceinline__ f32x4v load_cols4(const uint16_t* p) {
-  const uint2 r = *reinterpret_cast<const uint2*>(p);
-  return f32x4v{__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xffff0000u), __uint_as_float(r.y << 16),
-                __uint_as_float(r.y & 0xffff0000u)};
-}
-__device__ __forceinline__ f32x4v load_cols4(const float* p) { return *reinterpret_cast<const f32x4v*>(p); }
-
 // part: [splits][64][H] then [splits][64] bias sums; one split writes the results themselves
-template <typename XT>
 __global__ __launch_bounds__(kWgWaves * 64) void router_weight_grad(
-    const XT* __restrict__ x, const float* __restrict__ dl, const uint8_t* __restrict__ mask, int T, int H, int E,
+    const float* __restrict__ x, const float* __restrict__ dl, const uint8_t* __restrict__ mask, int T, int H, int E,
     int per_split, float* __restrict__ part, float* __restrict__ bias_part, float* __restrict__ d_wg,
     float* __restrict__ d_bias) {
   __shared__ float red[kWgWaves / 2][kMaxExperts][kWgCols];
@@ -394,7 +386,7 @@ __global__ __launch_bounds__(kWgWaves * 64) void router_weight_grad(
   for (int t0 = t_begin + wave * 4; t0 < t_end; t0 += kWgWaves * 4) {
     const int t = t0 + g, tc = min(t, t_end - 1);
     const bool ok = t < t_end && (mask == nullptr || mask[tc] != 0);
-    f32x4v b = load_cols4(x + (size_t)tc * H + h0 + 4 * l);
+    f32x4v b = *reinterpret_cast<const f32x4v*>(x + (size_t)tc * H + h0 + 4 * l);
     float a[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
@@ -467,6 +459,212 @@ __global__ __launch_bounds__(kWgWaves * 64) void router_weight_grad(
   }
 }
 
+// The same for bf16 x on v_mfma_f32_16x16x32_bf16, a block of 32 tokens x 64
+// columns per wave and step.  d_logits enter as three bf16 parts (the upper 8
+// bits of the significand, the next 8, the last 8: each difference is exact),
+// so a product is as exact as in fp32 at 3/16 of the fp32 matrix time.  Both
+// operands want a lane to hold 8 tokens of one column, and both lie in memory
+// token by token: a lane loads four neighbouring columns of its 8 tokens and
+// puts pairs of tokens together with byte permutations.  Column tile c then
+// holds columns 4 (lane%16) + c, and expert tile m holds experts
+// 4 (lane%16) + m (VEC: E % 4 == 0, 16-byte loads) or 16 m + lane%16.
+constexpr int kWbWaves = 8;
+constexpr int kWbTok = 32;  // tokens of a wave's step
+
+inline int wgrad_bf16_splits(int T, int H) {
+  return std::max(1, std::min(kWgBlocks / (H / kWgCols), (T + kWbWaves * kWbTok - 1) / (kWbWaves * kWbTok)));
+}
+
+// the upper halves of two words, and the lower halves
+__device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+__device__ __forceinline__ uint32_t pack_lo(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+
+struct WgBlock {
+  uint2 x[8];       // four columns of token 8 g + i
+  float d[8][4];    // four experts of it
+  uint32_t ok;      // bit i: token i counts
+};
+
+template <bool VEC, bool MASK>
+__global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
+    const uint16_t* __restrict__ x, const float* __restrict__ dl, const uint8_t* __restrict__ mask, int T, int H,
+    int E, int per_split, float* __restrict__ part, float* __restrict__ bias_part, float* __restrict__ d_wg,
+    float* __restrict__ d_bias) {
+  __shared__ __attribute__((aligned(16))) float red[kWbWaves / 2][kMaxExperts][kWgCols];
+  __shared__ float bred[kWbWaves][kMaxExperts];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l = lane & 15, g = lane >> 4;
+  const int split = blockIdx.y, h0 = blockIdx.x * kWgCols;
+  const int t_begin = split * per_split, t_end = min(T, t_begin + per_split);
+  auto expert = [&](int m) { return VEC ? 4 * l + m : 16 * m + l; };
+
+  auto load = [&](int t0, WgBlock& b) {
+    const int tb = t0 + 8 * g;
+    if (t0 + kWbTok <= t_end) {  // the same for the whole wave
+      b.ok = 0xffu;
+      if constexpr (MASK) {
+        const uint2 mv = *reinterpret_cast<const uint2*>(mask + tb);  // t0 % 8 == 0
+        b.ok = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          b.ok |= ((mv.x >> (8 * i) & 0xffu) != 0 ? 1u << i : 0u) | ((mv.y >> (8 * i) & 0xffu) != 0 ? 16u << i : 0u);
+      }
+    } else {
+      b.ok = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        b.ok |= tb + i < t_end && (!MASK || mask[min(tb + i, T - 1)] != 0) ? 1u << i : 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const size_t t = min(tb + i, T - 1);  // tokens past the end are dropped below
+      b.x[i] = *reinterpret_cast<const uint2*>(x + t * H + h0 + 4 * l);
+      if constexpr (VEC) {
+        const f32x4v v = *reinterpret_cast<const f32x4v*>(dl + t * E + min(4 * l, E - 4));
+#pragma unroll
+        for (int m = 0; m < 4; ++m) b.d[i][m] = v[m];
+      } else {
+#pragma unroll
+        for (int m = 0; m < 4; ++m) b.d[i][m] = dl[t * E + min(16 * m + l, E - 1)];
+      }
+    }
+  };
+
+  f32x4v acc[4][4];
+  float bsum[4] = {};
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[m][c] = f32x4v{0.f, 0.f, 0.f, 0.f};
+
+  auto products = [&](const WgBlock& b) {
+    uint2 xv[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool ok = (b.ok >> i & 1u) != 0;
+      xv[i] = make_uint2(ok ? b.x[i].x : 0u, ok ? b.x[i].y : 0u);
+    }
+    bf16x8 bx[4];  // column tile c
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 lo, hi;
+      lo.x = pack_lo(h ? xv[0].y : xv[0].x, h ? xv[1].y : xv[1].x);
+      lo.y = pack_lo(h ? xv[2].y : xv[2].x, h ? xv[3].y : xv[3].x);
+      lo.z = pack_lo(h ? xv[4].y : xv[4].x, h ? xv[5].y : xv[5].x);
+      lo.w = pack_lo(h ? xv[6].y : xv[6].x, h ? xv[7].y : xv[7].x);
+      hi.x = pack_hi(h ? xv[0].y : xv[0].x, h ? xv[1].y : xv[1].x);
+      hi.y = pack_hi(h ? xv[2].y : xv[2].x, h ? xv[3].y : xv[3].x);
+      hi.z = pack_hi(h ? xv[4].y : xv[4].x, h ? xv[5].y : xv[5].x);
+      hi.w = pack_hi(h ? xv[6].y : xv[6].x, h ? xv[7].y : xv[7].x);
+      bx[2 * h] = __builtin_bit_cast(bf16x8, lo);
+      bx[2 * h + 1] = __builtin_bit_cast(bf16x8, hi);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const bool live = expert(m) < E;
+      float v[8], r1[8], r2[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = live && (b.ok >> i & 1u) != 0 ? b.d[i][m] : 0.0f;
+        bsum[m] += v[i];
+        r1[i] = v[i] - __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
+        r2[i] = r1[i] - __uint_as_float(__float_as_uint(r1[i]) & 0xffff0000u);
+      }
+      auto pack8 = [](const float (&f)[8]) {
+        uint4 p;
+        p.x = pack_hi(__float_as_uint(f[0]), __float_as_uint(f[1]));
+        p.y = pack_hi(__float_as_uint(f[2]), __float_as_uint(f[3]));
+        p.z = pack_hi(__float_as_uint(f[4]), __float_as_uint(f[5]));
+        p.w = pack_hi(__float_as_uint(f[6]), __float_as_uint(f[7]));
+        return __builtin_bit_cast(bf16x8, p);
+      };
+      const bf16x8 a0 = pack8(v), a1 = pack8(r1), a2 = pack8(r2);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a2, bx[c], acc[m][c], 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, bx[c], acc[m][c], 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, bx[c], acc[m][c], 0, 0, 0);
+    }
+  };
+
+  // two blocks in turn, the next one's loads out before this one's products
+  constexpr int kStep = kWbWaves * kWbTok;
+  int t0 = t_begin + wave * kWbTok;
+  if (t0 < t_end) {
+    WgBlock b0, b1;
+    load(t0, b0);
+    while (true) {
+      if (t0 + kStep < t_end) load(t0 + kStep, b1);
+      __builtin_amdgcn_sched_barrier(0);
+      products(b0);
+      t0 += kStep;
+      if (t0 >= t_end) break;
+      if (t0 + kStep < t_end) load(t0 + kStep, b0);
+      __builtin_amdgcn_sched_barrier(0);
+      products(b1);
+      t0 += kStep;
+      if (t0 >= t_end) break;
+    }
+  }
+
+  // D layout: register r of a lane holds row 4 g + r of the expert tile, column l of the column tile
+  auto row = [&](int m, int r) { return VEC ? 4 * (4 * g + r) + m : 16 * m + 4 * g + r; };
+#pragma unroll
+  for (int half = kWbWaves / 2; half >= 1; half >>= 1) {
+    if (wave >= half && wave < 2 * half) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          *reinterpret_cast<f32x4v*>(&red[wave - half][row(m, r)][4 * l]) =
+              f32x4v{acc[m][0][r], acc[m][1][r], acc[m][2][r], acc[m][3][r]};
+    }
+    __syncthreads();
+    if (wave < half) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const f32x4v o = *reinterpret_cast<const f32x4v*>(&red[wave][row(m, r)][4 * l]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) acc[m][c][r] += o[c];
+        }
+    }
+    __syncthreads();
+  }
+  const bool last = gridDim.y == 1;
+  if (wave == 0) {
+    float* out = last ? d_wg : part + (size_t)split * kMaxExperts * H;
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (row(m, r) < E)
+          *reinterpret_cast<f32x4v*>(out + (size_t)row(m, r) * H + h0 + 4 * l) =
+              f32x4v{acc[m][0][r], acc[m][1][r], acc[m][2][r], acc[m][3][r]};
+  }
+  if (blockIdx.x != 0) return;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    float v = bsum[m];
+    v += __shfl_xor(v, 16);
+    v += __shfl_xor(v, 32);
+    if (g == 0) bred[wave][expert(m)] = v;
+  }
+  __syncthreads();
+  if (tid < kMaxExperts) {
+    float s = bred[0][tid];
+#pragma unroll
+    for (int w = 1; w < kWbWaves; ++w) s += bred[w][tid];
+    if (!last)
+      bias_part[split * kMaxExperts + tid] = s;
+    else if (d_bias != nullptr && tid < E)
+      d_bias[tid] = s;
+  }
+}
+
 // Sum of the splits, ascending; one thread per four columns.
 __global__ __launch_bounds__(256) void router_weight_sum(const float* __restrict__ part,
                                                          const float* __restrict__ bias_part, int splits, int H,
@@ -498,7 +696,7 @@ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 inline int balance_blocks(int T) { return std::max(1, std::min(kBalBlocks, ceil_div(T, kBalStep))); }
 
 inline size_t wgrad_workspace(const Shape& s) {
-  const size_t sp = (size_t)wgrad_splits(s.T, s.H);
+  const size_t sp = (size_t)(s.bf16 ? wgrad_bf16_splits(s.T, s.H) : wgrad_splits(s.T, s.H));
   return sp == 1 ? 256 : sp * kMaxExperts * ((size_t)s.H + 1) * 4;
 }
 
@@ -591,17 +789,26 @@ moe_status moe_router_weight_grad(const moe_shape* shape, const void* x, const f
   MOE_CHECK(check_ptr(x)); MOE_CHECK(check_ptr(d_logits));
   if (token_mask != nullptr) MOE_CHECK(check_ptr(token_mask));
   MOE_CHECK(check_workspace(workspace, workspace_bytes, moe_router_grad_workspace_size(shape)));
-  const int splits = moe::wgrad_splits(s.T, s.H);
-  const int per = moe::ceil_div(s.T, splits);
+  const int splits = s.bf16 ? moe::wgrad_bf16_splits(s.T, s.H) : moe::wgrad_splits(s.T, s.H);
+  int per = moe::ceil_div(s.T, splits);
   float* part = (float*)workspace;
   float* bpart = part + (size_t)splits * moe::kMaxExperts * s.H;
-  const dim3 grid(s.H / moe::kWgCols, splits), block(moe::kWgWaves * 64);
-  if (s.bf16)
-    hipLaunchKernelGGL(moe::router_weight_grad<uint16_t>, grid, block, 0, st, (const uint16_t*)x, d_logits, token_mask,
-                       s.T, s.H, s.E, per, part, bpart, d_wg, d_bias);
-  else
-    hipLaunchKernelGGL(moe::router_weight_grad<float>, grid, block, 0, st, (const float*)x, d_logits, token_mask, s.T,
-                       s.H, s.E, per, part, bpart, d_wg, d_bias);
+  const dim3 grid(s.H / moe::kWgCols, splits);
+  if (s.bf16) {
+    per = moe::ceil_div(per, moe::kWbTok) * moe::kWbTok;
+#define MOE_GO(VEC, MASK)                                                                                          \
+  hipLaunchKernelGGL((moe::router_weight_grad_bf16<VEC, MASK>), grid, dim3(moe::kWbWaves * 64), 0, st,             \
+                     (const uint16_t*)x, d_logits, token_mask, s.T, s.H, s.E, per, part, bpart, d_wg, d_bias)
+    const bool vec = s.E % 4 == 0;
+    if (vec && token_mask != nullptr) MOE_GO(true, true);
+    else if (vec) MOE_GO(true, false);
+    else if (token_mask != nullptr) MOE_GO(false, true);
+    else MOE_GO(false, false);
+#undef MOE_GO
+  } else {
+    hipLaunchKernelGGL(moe::router_weight_grad, grid, dim3(moe::kWgWaves * 64), 0, st, (const float*)x, d_logits,
+                       token_mask, s.T, s.H, s.E, per, part, bpart, d_wg, d_bias);
+  }
   if (splits > 1)
     hipLaunchKernelGGL(moe::router_weight_sum, dim3(moe::ceil_div(s.E * s.H / 4, 256)), dim3(256), 0, st, part, bpart,
                        splits, s.H, s.E, d_wg, d_bias);

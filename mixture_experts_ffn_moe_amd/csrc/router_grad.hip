@@ -459,175 +459,223 @@ __global__ __launch_bounds__(kWgWaves * 64) void router_weight_grad(
   }
 }
 
-// The same for bf16 x on v_mfma_f32_16x16x32_bf16, a block of 32 tokens x 64
-// columns per wave and step.  d_logits enter as three bf16 parts (the upper 8
-// bits of the significand, the next 8, the last 8: each difference is exact),
-// so a product is as exact as in fp32 at 3/16 of the fp32 matrix time.  Both
-// operands want a lane to hold 8 tokens of one column, and both lie in memory
-// token by token: a lane loads four neighbouring columns of its 8 tokens and
-// puts pairs of tokens together with byte permutations.  Column tile c then
-// holds columns 4 (lane%16) + c, and expert tile m holds experts
-// 4 (lane%16) + m (VEC: E % 4 == 0, 16-byte loads) or 16 m + lane%16.
+// The same for bf16 x on v_mfma_f32_16x16x32_bf16.  d_logits enter as three
+// bf16 parts (the upper 8 bits of the significand, the next 8, the last 8:
+// each difference is exact), so a product is as exact as in fp32 at 3/16 of
+// the fp32 matrix time.  A workgroup of 8 waves takes CG x 64 columns and, per
+// step, TG x 32 tokens (CG TG = 8), a wave 64 columns of 32 tokens.
+// d_logits of a step are cut once per workgroup, by all of its threads, and
+// passed through LDS in operand order, one step ahead.  (Cut by every wave
+// for itself, the vector instructions took most of the time: 183 against 86 us
+// at 32767 tokens.)  x wants a lane to hold 8 tokens of one column and lies in
+// memory token by token: a lane loads four neighbouring columns of its 8
+// tokens and puts pairs of tokens together with byte permutations; column tile
+// c then holds columns 4 (lane%16) + c.
+// Few column groups mean few partial sums (a workgroup writes 64 experts x its
+// columns), many of them that d_logits are cut and read less often.
 constexpr int kWbWaves = 8;
 constexpr int kWbTok = 32;  // tokens of a wave's step
 
+inline int wgrad_groups(int T) { return T >= 16384 ? 4 : 2; }
 inline int wgrad_bf16_splits(int T, int H) {
-  return std::max(1, std::min(kWgBlocks / (H / kWgCols), (T + kWbWaves * kWbTok - 1) / (kWbWaves * kWbTok)));
+  const int cg = wgrad_groups(T), cols = (H / kWgCols + cg - 1) / cg, step = kWbWaves / cg * kWbTok;
+  return std::max(1, std::min(kWgBlocks / cols, (T + 2 * step - 1) / (2 * step)));
 }
 
 // the upper halves of two words, and the lower halves
 __device__ __forceinline__ uint32_t pack_hi(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
 __device__ __forceinline__ uint32_t pack_lo(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 
-struct WgBlock {
-  uint2 x[8];       // four columns of token 8 g + i
-  float d[8][4];    // four experts of it
-  uint32_t ok;      // bit i: token i counts
-};
-
-template <bool VEC, bool MASK>
+template <int CG, bool MASK>
 __global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
     const uint16_t* __restrict__ x, const float* __restrict__ dl, const uint8_t* __restrict__ mask, int T, int H,
     int E, int per_split, float* __restrict__ part, float* __restrict__ bias_part, float* __restrict__ d_wg,
     float* __restrict__ d_bias) {
-  __shared__ __attribute__((aligned(16))) float red[kWbWaves / 2][kMaxExperts][kWgCols];
+  constexpr int TG = kWbWaves / CG;
+  constexpr int kStep = TG * kWbTok;              // tokens of a step
+  constexpr int kPieces = kStep / 8 / kWbWaves;   // (8 tokens of one expert) that a thread cuts per step
+  constexpr int kBuf = TG * 3 * 4 * 1024;         // [token group][part][expert tile][lane] x 16 bytes
+  constexpr int kRed = TG / 2 * CG * kMaxExperts * kWgCols * 4;  // the final sums, which reuse the buffers
+  __shared__ __attribute__((aligned(1024))) char lds[2 * kBuf > kRed ? 2 * kBuf : kRed];
   __shared__ float bred[kWbWaves][kMaxExperts];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l = lane & 15, g = lane >> 4;
-  const int split = blockIdx.y, h0 = blockIdx.x * kWgCols;
+  const int cg = wave % CG, tg = wave / CG;
+  const int split = blockIdx.y;
+  const int hc = blockIdx.x * CG + cg;            // column group; past the last it repeats it and stores nothing
+  const int h0 = min(hc, H / kWgCols - 1) * kWgCols;
   const int t_begin = split * per_split, t_end = min(T, t_begin + per_split);
-  auto expert = [&](int m) { return VEC ? 4 * l + m : 16 * m + l; };
 
-  auto load = [&](int t0, WgBlock& b) {
-    const int tb = t0 + 8 * g;
-    if (t0 + kWbTok <= t_end) {  // the same for the whole wave
-      b.ok = 0xffu;
-      if constexpr (MASK) {
-        const uint2 mv = *reinterpret_cast<const uint2*>(mask + tb);  // t0 % 8 == 0
-        b.ok = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          b.ok |= ((mv.x >> (8 * i) & 0xffu) != 0 ? 1u << i : 0u) | ((mv.y >> (8 * i) & 0xffu) != 0 ? 16u << i : 0u);
-      }
+  // byte i not 0: token tb + i counts (the tokens of a whole block are all
+  // below t_end).  Kept as loaded: decoding waits for the load.
+  auto valid = [&](int tb, bool whole) -> uint2 {
+    uint2 ok = make_uint2(0x01010101u, 0x01010101u);
+    if (whole) {
+      if constexpr (MASK) ok = *reinterpret_cast<const uint2*>(mask + tb);  // tb % 8 == 0
     } else {
-      b.ok = 0;
+      uint32_t b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = tb + i < t_end && (!MASK || mask[min(tb + i, T - 1)] != 0) ? 1u : 0u;
+      ok = make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
+    }
+    return ok;
+  };
+  auto counts = [](const uint2& ok, int i) { return ((i < 4 ? ok.x : ok.y) >> (8 * (i & 3)) & 0xffu) != 0; };
+
+  // d_logits of a step: thread (wave, lane) takes expert `lane` of the tokens
+  // 8 (wave + 8 j) .. + 7
+  struct Cut {
+    float v[kPieces][8];
+    uint2 ok[kPieces];
+  };
+  auto load_d = [&](int t0, Cut& b) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int tb = t0 + 8 * (wave + kWbWaves * j);
+      const bool whole = tb + 8 <= t_end;
+      b.ok[j] = valid(tb, whole);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float* row = dl + (size_t)min(tb + i, T - 1) * E;
+        b.v[j][i] = row[(uint32_t)min(lane, E - 1)];
+      }
+    }
+  };
+  float bsum = 0.0f;
+  auto cut_d = [&](const Cut& b, int buf) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int pc = wave + kWbWaves * j;
+      float v[8], r1[8], r2[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i] = lane < E && counts(b.ok[j], i) ? b.v[j][i] : 0.0f;
+        bsum += v[i];
+        r1[i] = v[i] - __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
+        r2[i] = r1[i] - __uint_as_float(__float_as_uint(r1[i]) & 0xffff0000u);
+      }
+      char* at = lds + buf * kBuf + (pc / 4 * 12 + lane / 16) * 1024 + (pc % 4 * 16 + lane % 16) * 16;
+      auto pack8 = [](const float (&f)[8]) {
+        return make_uint4(pack_hi(__float_as_uint(f[0]), __float_as_uint(f[1])),
+                          pack_hi(__float_as_uint(f[2]), __float_as_uint(f[3])),
+                          pack_hi(__float_as_uint(f[4]), __float_as_uint(f[5])),
+                          pack_hi(__float_as_uint(f[6]), __float_as_uint(f[7])));
+      };
+      *reinterpret_cast<uint4*>(at) = pack8(v);
+      *reinterpret_cast<uint4*>(at + 4096) = pack8(r1);
+      *reinterpret_cast<uint4*>(at + 8192) = pack8(r2);
+    }
+  };
+  // x of this wave's tokens of a step: a uniform row plus the lane's offset
+  struct Rows {
+    uint2 v[8], ok;
+  };
+  auto load_x = [&](int t0, Rows& b) {
+    const int tw = t0 + tg * kWbTok;
+    const bool whole = tw + kWbTok <= t_end;
+    b.ok = valid(tw + 8 * g, whole);
+    if (whole) {
+      const uint32_t off = ((uint32_t)(8 * g) * (uint32_t)H + (uint32_t)(h0 + 4 * l)) * 2u;
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        b.ok |= tb + i < t_end && (!MASK || mask[min(tb + i, T - 1)] != 0) ? 1u << i : 0u;
-    }
+        b.v[i] = *reinterpret_cast<const uint2*>((const char*)(x + (size_t)(tw + i) * H) + off);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const size_t t = min(tb + i, T - 1);  // tokens past the end are dropped below
-      b.x[i] = *reinterpret_cast<const uint2*>(x + t * H + h0 + 4 * l);
-      if constexpr (VEC) {
-        const f32x4v v = *reinterpret_cast<const f32x4v*>(dl + t * E + min(4 * l, E - 4));
-#pragma unroll
-        for (int m = 0; m < 4; ++m) b.d[i][m] = v[m];
-      } else {
-#pragma unroll
-        for (int m = 0; m < 4; ++m) b.d[i][m] = dl[t * E + min(16 * m + l, E - 1)];
-      }
+      for (int i = 0; i < 8; ++i)  // tokens past the end are dropped below
+        b.v[i] = *reinterpret_cast<const uint2*>(x + (size_t)min(tw + 8 * g + i, T - 1) * H + h0 + 4 * l);
     }
   };
 
   f32x4v acc[4][4];
-  float bsum[4] = {};
 #pragma unroll
   for (int m = 0; m < 4; ++m)
 #pragma unroll
     for (int c = 0; c < 4; ++c) acc[m][c] = f32x4v{0.f, 0.f, 0.f, 0.f};
 
-  auto products = [&](const WgBlock& b) {
-    uint2 xv[8];
+  auto products = [&](Rows& b, int buf) {
+    bool all = true;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const bool ok = (b.ok >> i & 1u) != 0;
-      xv[i] = make_uint2(ok ? b.x[i].x : 0u, ok ? b.x[i].y : 0u);
-    }
-    bf16x8 bx[4];  // column tile c
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint4 lo, hi;
-      lo.x = pack_lo(h ? xv[0].y : xv[0].x, h ? xv[1].y : xv[1].x);
-      lo.y = pack_lo(h ? xv[2].y : xv[2].x, h ? xv[3].y : xv[3].x);
-      lo.z = pack_lo(h ? xv[4].y : xv[4].x, h ? xv[5].y : xv[5].x);
-      lo.w = pack_lo(h ? xv[6].y : xv[6].x, h ? xv[7].y : xv[7].x);
-      hi.x = pack_hi(h ? xv[0].y : xv[0].x, h ? xv[1].y : xv[1].x);
-      hi.y = pack_hi(h ? xv[2].y : xv[2].x, h ? xv[3].y : xv[3].x);
-      hi.z = pack_hi(h ? xv[4].y : xv[4].x, h ? xv[5].y : xv[5].x);
-      hi.w = pack_hi(h ? xv[6].y : xv[6].x, h ? xv[7].y : xv[7].x);
-      bx[2 * h] = __builtin_bit_cast(bf16x8, lo);
-      bx[2 * h + 1] = __builtin_bit_cast(bf16x8, hi);
-    }
-#pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const bool live = expert(m) < E;
-      float v[8], r1[8], r2[8];
+    for (int i = 0; i < 8; ++i) all = all && counts(b.ok, i);
+    if (__any(!all)) {  // rows that do not count may hold anything
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] = live && (b.ok >> i & 1u) != 0 ? b.d[i][m] : 0.0f;
-        bsum[m] += v[i];
-        r1[i] = v[i] - __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
-        r2[i] = r1[i] - __uint_as_float(__float_as_uint(r1[i]) & 0xffff0000u);
+        const bool ok = counts(b.ok, i);
+        b.v[i] = make_uint2(ok ? b.v[i].x : 0u, ok ? b.v[i].y : 0u);
       }
-      auto pack8 = [](const float (&f)[8]) {
-        uint4 p;
-        p.x = pack_hi(__float_as_uint(f[0]), __float_as_uint(f[1]));
-        p.y = pack_hi(__float_as_uint(f[2]), __float_as_uint(f[3]));
-        p.z = pack_hi(__float_as_uint(f[4]), __float_as_uint(f[5]));
-        p.w = pack_hi(__float_as_uint(f[6]), __float_as_uint(f[7]));
-        return __builtin_bit_cast(bf16x8, p);
-      };
-      const bf16x8 a0 = pack8(v), a1 = pack8(r1), a2 = pack8(r2);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a2, bx[c], acc[m][c], 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a1, bx[c], acc[m][c], 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a0, bx[c], acc[m][c], 0, 0, 0);
     }
+    bf16x8 bx[4];  // column tile c
+    bx[0] = __builtin_bit_cast(bf16x8, make_uint4(pack_lo(b.v[0].x, b.v[1].x), pack_lo(b.v[2].x, b.v[3].x),
+                                                  pack_lo(b.v[4].x, b.v[5].x), pack_lo(b.v[6].x, b.v[7].x)));
+    bx[1] = __builtin_bit_cast(bf16x8, make_uint4(pack_hi(b.v[0].x, b.v[1].x), pack_hi(b.v[2].x, b.v[3].x),
+                                                  pack_hi(b.v[4].x, b.v[5].x), pack_hi(b.v[6].x, b.v[7].x)));
+    bx[2] = __builtin_bit_cast(bf16x8, make_uint4(pack_lo(b.v[0].y, b.v[1].y), pack_lo(b.v[2].y, b.v[3].y),
+                                                  pack_lo(b.v[4].y, b.v[5].y), pack_lo(b.v[6].y, b.v[7].y)));
+    bx[3] = __builtin_bit_cast(bf16x8, make_uint4(pack_hi(b.v[0].y, b.v[1].y), pack_hi(b.v[2].y, b.v[3].y),
+                                                  pack_hi(b.v[4].y, b.v[5].y), pack_hi(b.v[6].y, b.v[7].y)));
+    const char* frag = lds + buf * kBuf + tg * 12 * 1024 + (g * 16 + l) * 16;
+#pragma unroll
+    for (int q = 2; q >= 0; --q)  // smallest part first
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const bf16x8 a = *reinterpret_cast<const bf16x8*>(frag + (q * 4 + m) * 1024);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, bx[c], acc[m][c], 0, 0, 0);
+      }
+  };
+  auto barrier = [] {  // orders LDS accesses, leaves loads in flight
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
   };
 
-  // two blocks in turn, the next one's loads out before this one's products
-  constexpr int kStep = kWbWaves * kWbTok;
-  int t0 = t_begin + wave * kWbTok;
-  if (t0 < t_end) {
-    WgBlock b0, b1;
-    load(t0, b0);
-    while (true) {
-      if (t0 + kStep < t_end) load(t0 + kStep, b1);
+  // Step s: its x and cut d_logits are here; the next step's d_logits are cut
+  // meanwhile, and the loads of the one after it go out.
+  const int steps = t_end > t_begin ? (t_end - t_begin + kStep - 1) / kStep : 0;
+  if (steps > 0) {
+    Rows x0, x1;
+    Cut d;
+    load_d(t_begin, d);
+    load_x(t_begin, x0);
+    cut_d(d, 0);
+    load_d(min(t_begin + kStep, t_end - 1) / 8 * 8, d);
+    load_x(min(t_begin + kStep, t_end - 1) / 8 * 8, x1);
+    barrier();
+    auto step = [&](int s, Rows& cur) {
+      products(cur, s & 1);
+      if (s + 1 < steps) cut_d(d, (s + 1) & 1);
+      if (s + 2 < steps) {
+        load_d(t_begin + (s + 2) * kStep, d);
+        load_x(t_begin + (s + 2) * kStep, cur);
+      }
       __builtin_amdgcn_sched_barrier(0);
-      products(b0);
-      t0 += kStep;
-      if (t0 >= t_end) break;
-      if (t0 + kStep < t_end) load(t0 + kStep, b0);
-      __builtin_amdgcn_sched_barrier(0);
-      products(b1);
-      t0 += kStep;
-      if (t0 >= t_end) break;
+      barrier();
+    };
+    for (int s = 0; s < steps; s += 2) {
+      step(s, x0);
+      if (s + 1 < steps) step(s + 1, x1);
     }
   }
 
   // D layout: register r of a lane holds row 4 g + r of the expert tile, column l of the column tile
-  auto row = [&](int m, int r) { return VEC ? 4 * (4 * g + r) + m : 16 * m + 4 * g + r; };
+  float(*red)[kMaxExperts][kWgCols] = reinterpret_cast<float(*)[kMaxExperts][kWgCols]>(lds);
 #pragma unroll
-  for (int half = kWbWaves / 2; half >= 1; half >>= 1) {
-    if (wave >= half && wave < 2 * half) {
+  for (int half = TG / 2; half >= 1; half >>= 1) {
+    if (tg >= half && tg < 2 * half) {
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          *reinterpret_cast<f32x4v*>(&red[wave - half][row(m, r)][4 * l]) =
+          *reinterpret_cast<f32x4v*>(&red[(tg - half) * CG + cg][16 * m + 4 * g + r][4 * l]) =
               f32x4v{acc[m][0][r], acc[m][1][r], acc[m][2][r], acc[m][3][r]};
     }
     __syncthreads();
-    if (wave < half) {
+    if (tg < half) {
 #pragma unroll
       for (int m = 0; m < 4; ++m)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          const f32x4v o = *reinterpret_cast<const f32x4v*>(&red[wave][row(m, r)][4 * l]);
+          const f32x4v o = *reinterpret_cast<const f32x4v*>(&red[tg * CG + cg][16 * m + 4 * g + r][4 * l]);
 #pragma unroll
           for (int c = 0; c < 4; ++c) acc[m][c][r] += o[c];
         }
@@ -635,24 +683,18 @@ __global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
     __syncthreads();
   }
   const bool last = gridDim.y == 1;
-  if (wave == 0) {
+  if (tg == 0 && hc < H / kWgCols) {
     float* out = last ? d_wg : part + (size_t)split * kMaxExperts * H;
 #pragma unroll
     for (int m = 0; m < 4; ++m)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (row(m, r) < E)
-          *reinterpret_cast<f32x4v*>(out + (size_t)row(m, r) * H + h0 + 4 * l) =
+        if (16 * m + 4 * g + r < E)
+          *reinterpret_cast<f32x4v*>(out + (size_t)(16 * m + 4 * g + r) * H + h0 + 4 * l) =
               f32x4v{acc[m][0][r], acc[m][1][r], acc[m][2][r], acc[m][3][r]};
   }
   if (blockIdx.x != 0) return;
-#pragma unroll
-  for (int m = 0; m < 4; ++m) {
-    float v = bsum[m];
-    v += __shfl_xor(v, 16);
-    v += __shfl_xor(v, 32);
-    if (g == 0) bred[wave][expert(m)] = v;
-  }
+  bred[wave][lane] = bsum;
   __syncthreads();
   if (tid < kMaxExperts) {
     float s = bred[0][tid];
@@ -793,20 +835,20 @@ moe_status moe_router_weight_grad(const moe_shape* shape, const void* x, const f
   int per = moe::ceil_div(s.T, splits);
   float* part = (float*)workspace;
   float* bpart = part + (size_t)splits * moe::kMaxExperts * s.H;
-  const dim3 grid(s.H / moe::kWgCols, splits);
   if (s.bf16) {
+    const int cg = moe::wgrad_groups(s.T);
+    const dim3 grid(moe::ceil_div(s.H / moe::kWgCols, cg), splits);
     per = moe::ceil_div(per, moe::kWbTok) * moe::kWbTok;
-#define MOE_GO(VEC, MASK)                                                                                          \
-  hipLaunchKernelGGL((moe::router_weight_grad_bf16<VEC, MASK>), grid, dim3(moe::kWbWaves * 64), 0, st,             \
+#define MOE_GO(CG, MASK)                                                                                           \
+  hipLaunchKernelGGL((moe::router_weight_grad_bf16<CG, MASK>), grid, dim3(moe::kWbWaves * 64), 0, st,              \
                      (const uint16_t*)x, d_logits, token_mask, s.T, s.H, s.E, per, part, bpart, d_wg, d_bias)
-    const bool vec = s.E % 4 == 0;
-    if (vec && token_mask != nullptr) MOE_GO(true, true);
-    else if (vec) MOE_GO(true, false);
-    else if (token_mask != nullptr) MOE_GO(false, true);
-    else MOE_GO(false, false);
+    if (cg == 4 && token_mask != nullptr) MOE_GO(4, true);
+    else if (cg == 4) MOE_GO(4, false);
+    else if (token_mask != nullptr) MOE_GO(2, true);
+    else MOE_GO(2, false);
 #undef MOE_GO
   } else {
-    hipLaunchKernelGGL(moe::router_weight_grad, grid, dim3(moe::kWgWaves * 64), 0, st, (const float*)x, d_logits,
+    hipLaunchKernelGGL(moe::router_weight_grad, dim3(s.H / moe::kWgCols, splits), dim3(moe::kWgWaves * 64), 0, st, (const float*)x, d_logits,
                        token_mask, s.T, s.H, s.E, per, part, bpart, d_wg, d_bias);
   }
   if (splits > 1)

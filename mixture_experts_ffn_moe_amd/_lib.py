@@ -165,6 +165,8 @@ def _arg(name: str, t, dtype: torch.dtype, numel: int, nullable: bool = False):
     """Check one tensor argument against the element type and element count
     the C entry point will read or write through its raw pointer (the library
     cannot check sizes itself), then return the pointer."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype == dtype and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
         if nullable:
             return None
@@ -195,6 +197,8 @@ def y_nbytes(shape, rows: int) -> int:
 
 def _arg_bytes(name: str, t, nbytes: int):
     """A contiguous GPU tensor of exactly nbytes bytes (any element type)."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.numel() * t.element_size() == nbytes and t.is_contiguous():
+        return t.data_ptr()
     if t is None:
         raise ValueError(f"{name}: a tensor is required")
     if not isinstance(t, torch.Tensor):
@@ -206,10 +210,16 @@ def _arg_bytes(name: str, t, nbytes: int):
     return _ptr(t)
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+# the current stream's handle without a Stream object (which costs as much as a small launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(code: int, where: str):
@@ -361,10 +371,10 @@ def moe_forward_shared(shape, Is, x, wg, bias, w1, w2, w1s, w2s, out, workspace,
 
 
 def _on_current(*tensors):
-    """The library launches on the current device: every tensor has to be on it."""
+    """The library launches on the current device: every (GPU) tensor has to be on it."""
     here = torch.cuda.current_device()
     for t in tensors:
-        if isinstance(t, torch.Tensor) and t.device.type == "cuda" and t.device.index != here:
+        if t is not None and t.get_device() != here:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
 
 

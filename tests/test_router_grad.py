@@ -449,12 +449,13 @@ def test_refusals(m):
 
 
 def test_workspaces_stay_small(m):
-    """At most 256 partial sums whatever the shape."""
+    """At most 256 workgroups' sums whatever the shape: 768 bytes + padding each for the loss, 64 experts x 256
+    columns for the weight."""
     for T in (1, 64, 65, 4096, 60000):
         for H in (64, 448, 4096):
             s = m.make_shape(T, H, 64, 8, 32, 1, "bf16")
             assert 0 < m.moe_balance_workspace_size(s) <= 256 * 1024
-            assert 0 < m.moe_router_grad_workspace_size(s) <= 5 << 20
+            assert 0 < m.moe_router_grad_workspace_size(s) <= 17 << 20
 
 
 def test_binding_checks(m):

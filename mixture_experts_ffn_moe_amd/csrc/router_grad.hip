@@ -21,11 +21,19 @@ namespace {
 constexpr int kTokWave = 4;
 constexpr int kPer = kMaxExperts / 16;  // experts per lane
 
+// Reduction over 16 lanes, the same bits in each of them: rotations within the
+// row by 8, 4, 2 and 1 (DPP: no LDS round trip, of which a token would wait for
+// sixteen in turn).
+template <int CTRL, typename F>
+__device__ __forceinline__ float row_step(float v, F f) {
+  return f(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true)));
+}
 template <typename F>
 __device__ __forceinline__ float row16_reduce(float v, F f) {
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) v = f(v, __shfl_xor(v, d));
-  return v;
+  v = row_step<0x128>(v, f);  // row_ror:8
+  v = row_step<0x124>(v, f);
+  v = row_step<0x122>(v, f);
+  return row_step<0x121>(v, f);
 }
 __device__ __forceinline__ float row16_sum(float v) {
   return row16_reduce(v, [](float a, float b) { return a + b; });
@@ -99,17 +107,29 @@ __global__ __launch_bounds__(kBalWaves * 64) void balance_partial(
 
   double sum[kPer] = {};
   int valid = 0;
-  for (int t0 = t_begin; t0 < t_end; t0 += kBalStep) {
-    const int t = t0 + wave * kTokWave + g;
-    const int tc = min(t, t_end - 1);
-    const bool ok = t < t_end && (mask == nullptr || mask[tc] != 0);
-    float v[kPer], p[kPer];
+  // four steps' loads are in flight before the first is used (256 tokens, a
+  // workgroup's share at 65536)
+  constexpr int kAhead = 4;
+  for (int t0 = t_begin; t0 < t_end; t0 += kAhead * kBalStep) {
+    float v[kAhead][kPer];
+    uint8_t mk[kAhead];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = logits[(size_t)tc * E + min(l + 16 * i, E - 1)];
-    softmax16(v, l, E, ok, p);
+    for (int u = 0; u < kAhead; ++u) {
+      const int tc = min(t0 + u * kBalStep + wave * kTokWave + g, t_end - 1);
+      mk[u] = mask != nullptr ? mask[tc] : (uint8_t)1;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) sum[i] += (double)p[i];
-    valid += (ok && l == 0) ? 1 : 0;
+      for (int i = 0; i < kPer; ++i) v[u][i] = logits[(size_t)tc * E + min(l + 16 * i, E - 1)];
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      if (t0 + u * kBalStep >= t_end) break;
+      const bool ok = t0 + u * kBalStep + wave * kTokWave + g < t_end && mk[u] != 0;
+      float p[kPer];
+      softmax16(v[u], l, E, ok, p);
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) sum[i] += (double)p[i];
+      valid += (ok && l == 0) ? 1 : 0;
+    }
   }
   for (int r = t_begin * k + tid; r < t_end * k; r += kBalWaves * 64) {
     const int e = ids[r];
@@ -148,10 +168,23 @@ __global__ __launch_bounds__(kBalWaves * 64) void balance_finish(const BalancePa
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   double s = 0.0;
   int c = 0, n = 0;
-  for (int b = wave; b < nb; b += kBalWaves) {
-    s += partial[b].prob[lane];
-    c += partial[b].count[lane];
-    n += partial[b].valid;
+  for (int b = wave; b < nb; b += 4 * kBalWaves) {  // four partials in flight
+    double pv[4];
+    int cv[4], nv[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const BalancePartial& q = partial[min(b + u * kBalWaves, nb - 1)];
+      pv[u] = q.prob[lane];
+      cv[u] = q.count[lane];
+      nv[u] = q.valid;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool in = b + u * kBalWaves < nb;
+      s += in ? pv[u] : 0.0;
+      c += in ? cv[u] : 0;
+      n += in ? nv[u] : 0;
+    }
   }
   prob[wave][lane] = s;
   cnt[wave][lane] = c;
@@ -204,10 +237,21 @@ __global__ __launch_bounds__(kRbWaves * 64) void route_backward(
     const int tc = min(t, T - 1);
     const bool ok = t < T && (mask == nullptr || mask[tc] != 0);
     float p[kPer] = {}, d[kPer] = {};
+    // the first 16 routes' values beside the logits (k is 8, mostly); more of
+    // them are read again below
+    const size_t r0 = (size_t)tc * k + min(l, k - 1);
+    float w0 = 0.0f, dw0 = 0.0f, v[kPer] = {};
+    int e0 = -1;
     if (need_p) {
-      float v[kPer];
 #pragma unroll
       for (int i = 0; i < kPer; ++i) v[i] = logits[(size_t)tc * E + min(l + 16 * i, E - 1)];
+    }
+    if (d_w != nullptr) {
+      w0 = topw[r0];
+      dw0 = d_w[r0];
+      e0 = ids[r0];
+    }
+    if (need_p) {
       softmax16(v, l, E, ok, p);
       float fp = 0.0f;
 #pragma unroll
@@ -219,14 +263,15 @@ __global__ __launch_bounds__(kRbWaves * 64) void route_backward(
     if (d_w != nullptr) {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) row[l + 16 * i] = 0.0f;
-      float dot = 0.0f;
-      for (int j = l; j < k; j += 16) {
+      float dot = l < k ? w0 * dw0 : 0.0f;
+      for (int j = l + 16; j < k; j += 16) {
         const size_t r = (size_t)tc * k + j;
         dot = fmaf(topw[r], d_w[r], dot);
       }
       dot = row16_sum(dot);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      for (int j = l; j < k; j += 16) {
+      if (l < k && (unsigned)e0 < (unsigned)E) row[e0] = renorm ? w0 * (dw0 - dot) : dw0;
+      for (int j = l + 16; j < k; j += 16) {
         const size_t r = (size_t)tc * k + j;
         const int e = ids[r];
         if ((unsigned)e < (unsigned)E) row[e] = renorm ? topw[r] * (d_w[r] - dot) : d_w[r];

@@ -47,12 +47,28 @@ __device__ __forceinline__ bf16x8 q4_operand(uint32_t w, const Q4Consts& k) {
   return __builtin_bit_cast(bf16x8, r);
 }
 
+// 16 bytes a lane of a code tile.
+template <bool NONTEMPORAL>
+__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
+  if constexpr (NONTEMPORAL) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
+  } else {
+    return *reinterpret_cast<const uint4*>(p);
+  }
+}
+
 // Element i of an operand as the fp32 value of its code (exact).
 template <int FMT>
 __device__ __forceinline__ float q4_value(const bf16x8& b, int i) {
   const float v = (float)b[i];
   return FMT == kQ4Int ? v - 136.0f : v;
 }
+
+// Keeps the additions that produce v in this block.  (The compiler may sink
+// them past a branch, right behind the matrix instruction whose result they
+// read, and then leaves out the wait states that this instruction needs.)
+__device__ __forceinline__ void pin(f32x4& v) { asm volatile("" : "+v"(v)); }
 
 // Sum of v over the 4, 8 or 16 neighbouring lanes that hold one group (DPP: no
 // LDS round trip; mirrors do after the first two steps, whose sums are equal
@@ -70,13 +86,16 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return v;
 }
 
-// Sum of 8 bf16 values, then over the lanes of one group (16 / GPB chunks of 8).
+// -136 times the sum of 8 bf16 values, then over the lanes of one group (16 / GPB
+// chunks of 8): what the accumulator of an INT4 group starts at.
 template <int GPB>
-__device__ __forceinline__ float q4_group_sum(const uint4& v) {
+__device__ __forceinline__ float q4_group_start(const uint4& v) {
+  const bf16x2 c = __builtin_bit_cast(bf16x2, 0xc308c308u);  // -136, twice
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   float s = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) s += __uint_as_float(w[j] << 16) + __uint_as_float(w[j] & 0xffff0000u);
+  for (int j = 0; j < 4; ++j) s = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w[j]), c, s, false);
+  asm volatile("" : "+v"(s));  // the reader below stays in this block (the wait states that the product needs)
   return lanes_sum<16 / GPB>(s);
 }
 

@@ -18,7 +18,9 @@
 //      zeros), so one accumulator gathers w[t, j] * y over all experts of a
 //      wave and the 16 waves' sums are the output.
 // Both keep 8 KB of codes in flight per wave (128 KB a CU) and issue a tile's
-// successor as soon as its registers are free.
+// successor as soon as its registers are free.  The loads are nontemporal (the
+// layer at T = 8: 64.5 against 67.9 us in the kernel trace, at T = 16 with
+// groups of 32: 92 against 100 us).
 #include "decode_route.h"
 #include "q4.h"
 
@@ -45,13 +47,6 @@ struct Q4DecodeArgs {
   float* topw;
   int32_t *counts, *offsets, *perm, *inv, *active;
 };
-
-// Codes are read once: nontemporal loads (the layer at T = 8: 64.5 against 67.9
-// us in the kernel trace, at T = 16 with groups of 32: 92 against 100 us).
-__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
-  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  return __builtin_bit_cast(uint4, __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p)));
-}
 
 // Scales stay as loaded (bf16, two a word): a conversion would wait for the
 // loads where they are issued.
@@ -90,11 +85,6 @@ __device__ __forceinline__ float half_scale(uint32_t w, int i) {
   return __uint_as_float((i & 1) ? w & 0xffff0000u : w << 16);
 }
 
-// Keeps the additions that produce v in this block.  (The compiler may sink
-// them past a branch, right behind the matrix instruction whose result they
-// read, and then leaves out the wait states that this instruction needs.)
-__device__ __forceinline__ void pin(f32x4& v) { asm volatile("" : "+v"(v)); }
-
 // One 128-column tile: a group's sum on the matrix pipe, from start(group) on,
 // then times its scale.  INT4 operands are 128 + code: their sums start at
 // -136 times the rows' sums over the group.
@@ -113,14 +103,6 @@ __device__ __forceinline__ void tile_mma(const uint4& c, const float (&s)[GPB], 
     for (int r = 0; r < 4; ++r) acc[r] = fmaf(s[gr], part[r], acc[r]);
   }
   pin(acc);
-}
-
-// A barrier that orders LDS accesses and leaves loads in flight (the one of
-// __syncthreads waits for them).
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 constexpr int kDqStage = (int)(kDqMaxRows / 16 / (kDqWaves * 64));  // 16-byte chunks a thread stages, at most
@@ -156,8 +138,8 @@ __global__ __launch_bounds__(kDqWaves * 64) void q4_decode_w13(Q4DecodeArgs a) {
         const int t = q0 / (a.H / 8), c = q0 - t * (a.H / 8) + lane;
         *reinterpret_cast<uint4*>(xl + (t * (a.H / 8) + (c ^ t)) * 16) = xv[i];
         if constexpr (FMT == kQ4Int) {
-          const float sum = q4_group_sum<GPB>(xv[i]);
-          if ((lane & (16 / GPB - 1)) == 0) xsum[c / (16 / GPB) * Tp + t] = -136.0f * sum;
+          const float sum = q4_group_start<GPB>(xv[i]);
+          if ((lane & (16 / GPB - 1)) == 0) xsum[c / (16 / GPB) * Tp + t] = sum;
         }
       }
     }
@@ -209,7 +191,7 @@ __global__ __launch_bounds__(kDqWaves * 64) void q4_decode_w13(Q4DecodeArgs a) {
   uint4 ring[kDqRing];
   uint32_t rsc[kDqRing / 4][2 * GPB];
   auto load_tile = [&](const Seg& sg, int kb, int i) {
-    ring[i] = load_codes(sg.cp + (size_t)(kb + i) * kQ4TileBytes);
+    ring[i] = load_codes<true>(sg.cp + (size_t)(kb + i) * kQ4TileBytes);
     if ((i & 3) == 3) load_step_scales<GPB>(sg.sp + (kb + i - 3) * GPB, rsc[i / 4]);
   };
   auto store_h = [&](int e, int col, const f32x4& v) {
@@ -391,7 +373,7 @@ __global__ __launch_bounds__(kDqWaves * 64) void q4_decode_down(Q4DownArgs a) {
     uint4 ring[kDqRing];
     uint32_t rsc[kDqRing][(GPB + 1) / 2];
     auto load_tile = [&](int i) {
-      ring[i] = load_codes(lc + (size_t)lkb * kQ4TileBytes);
+      ring[i] = load_codes<true>(lc + (size_t)lkb * kQ4TileBytes);
       load_tile_scales<GPB>(lsc + lkb * GPB, rsc[i]);
       if (lq + 1 < q1) {
         ++lq;

@@ -17,13 +17,14 @@
 // row's own line.  Four steps' scales are therefore loaded at once, each of the
 // four lane groups taking one step's, and handed to the other groups by a lane
 // permutation.  (Loaded step by step they were fetched anew each time, more
-// lines than the L1 holds: 168 against 121 us for the gate|up product at 256
+// lines than the L1 holds: 168 against 144 us for the gate|up product at 256
 // tokens, two micro-shards.)
 //
 // INT4 codes enter as 128 + code (q4.h).  The 136 * sum(x) too much of a
 // group is the same for every weight row: each wave sums the chunks that it
-// copied itself (8 values, then over the group's lanes), and -136 times the
-// sum starts the group's accumulator: no extra matrix instruction.
+// copied itself (8 values on the two-element dot product, then over the group's
+// lanes), and -136 times the sum starts the group's accumulator: no extra
+// matrix instruction.
 #pragma once
 
 #include "q4.h"
@@ -83,18 +84,6 @@ constexpr int kQrTiles = 2;         // weight row tiles of a wave
 constexpr int kQrColTiles = kQrWaves * kQrTiles;
 constexpr int kQrLds = 65536;       // bytes of the staged rows' slots, at most
 
-// An LDS barrier that leaves loads in flight.
-__device__ __forceinline__ void q4_lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// Keeps the additions that produce v in this block: sunk past a branch, right
-// behind the matrix instruction whose result they read, they have been left
-// without the wait states that this instruction needs.
-__device__ __forceinline__ void q4_pin(f32x4& v) { asm volatile("" : "+v"(v)); }
-
 // One direct-to-LDS load of 16 bytes a lane from a 64-bit address (rows whose
 // offsets pass 32 bits); otherwise as dma16.
 __device__ __forceinline__ void dma16_at(uint32_t lds, const void* p) {
@@ -138,15 +127,14 @@ struct RowsBody {
   char* abuf;
   float* xsum;    // [slot][group][row]
   const int tid, lane, wave, fr, g, tile0;
-  int lseg = 0, lkb = 0;    // the step to load next (columns past the matrix's last tile: empty steps)
-  int KBp;                  // steps of a segment, a multiple of D
+  int lseg = 0, lkb = 0;    // the step to load next
   const Q4Consts kc;
 
   // Addresses are a uniform base (scalar registers) plus a 32-bit offset of the lane.
   const uint8_t* codes[NT];
   const XT* scales[NT];
   size_t seg_codes, seg_scales;
-  uint32_t code_off, scale_off;
+  uint32_t code_off;
   size_t src[kCopies];      // byte offset of the row a copy's lane reads
   int col[kCopies];         // and its column within the tile
   uint4 cw[D][NT];
@@ -170,8 +158,6 @@ struct RowsBody {
       scales[n] = (const XT*)a.scales + tile * 16 * a.S;
     }
     code_off = lane * 16;
-    scale_off = (uint32_t)((fr * a.S + g * GPB) * (int)sizeof(XT));
-    KBp = (a.KB + D - 1) / D * D;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
       // chunk q of the slot holds chunk (q % kChunks) ^ swizzle of row q / kChunks
@@ -187,11 +173,16 @@ struct RowsBody {
       for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
 
+  // Nontemporal for the gate|up product (256 tokens, two micro-shards: 136
+  // against 145 us; T = 64: 54 against 57 us, T = 1024: 188 against 190 us): the
+  // rows stay in the L2.  Not for the down product, whose rows are fewer (T =
+  // 256: 47 against 48 us, T = 1024: 126 against 130 us).
+  //
   // A step is 128 columns, tile kb of segment seg: its rows to the slot, its
-  // codes to registers, and on to the step after it.  An empty step loads the
-  // segment's last tile again.
+  // codes to registers, and on to the step after it.  Past the last step that
+  // one is loaded again, and not used.
   __device__ __forceinline__ void next(int slot, uint4 (&c)[NT]) {
-    const int kb = min(lkb, a.KB - 1), seg = W13 ? 0 : lseg, k0 = kb * kQ4TileK;
+    const int kb = lkb, seg = W13 ? 0 : lseg, k0 = kb * kQ4TileK;
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
       // columns past the matrix meet codes and scales of zero: the row's first columns will do
@@ -204,17 +195,27 @@ struct RowsBody {
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      c[n] = *reinterpret_cast<const uint4*>(codes[n] + seg * seg_codes + (size_t)kb * kQ4TileBytes + code_off);
-    const bool wrap = lkb + 1 == KBp;
-    lkb = wrap ? 0 : lkb + 1;
-    lseg = wrap ? lseg + 1 : lseg;
+      c[n] = load_codes<W13>(codes[n] + seg * seg_codes + (size_t)kb * kQ4TileBytes + code_off);
+    const bool wrap = lkb + 1 == a.KB, end = wrap && lseg + 1 == a.segments;
+    lkb = end ? lkb : wrap ? 0 : lkb + 1;
+    lseg += wrap && !end ? 1 : 0;
   }
-  // The scales of the D steps from the next one on.
+  // The scales of the D steps from the next one on, lane group g's of step g
+  // (steps past the last: any of the matrix's, not used).
   __device__ __forceinline__ void next_scales() {
-    const int seg = W13 ? 0 : lseg;
+    int k = lkb + g, seg = lseg;
+    if constexpr (!W13) {
+#pragma unroll
+      for (int i = 0; i + 1 < D; ++i) {  // a segment may be a single step
+        const bool wrap = k >= a.KB && seg + 1 < a.segments;
+        k -= wrap ? a.KB : 0;
+        seg += wrap ? 1 : 0;
+      }
+    }
+    const size_t off = (W13 ? (size_t)0 : seg * seg_scales) + (size_t)(uint32_t)(fr * a.S + min(k, a.KB - 1) * GPB);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      const char* p = (const char*)(scales[n] + seg * seg_scales + lkb * GPB) + scale_off;
+      const XT* p = scales[n] + off;
       if constexpr (kScaleBytes == 2) {
         snext[n][0] = *reinterpret_cast<const uint16_t*>(p);
       } else if constexpr (kScaleBytes == 4) {
@@ -239,9 +240,9 @@ struct RowsBody {
       for (int i = 0; i < kCopies; ++i) {
         const int q = (i * kQrWaves + wave) * 64 + lane, r = q / kChunks;
         // the xor swizzle permutes a row's groups and the chunks within one
-        const float s = q4_group_sum<GPB>(*reinterpret_cast<const uint4*>(abuf + slot * kSlot + q * 16));
+        const float s = q4_group_start<GPB>(*reinterpret_cast<const uint4*>(abuf + slot * kSlot + q * 16));
         const int c = (lane & 15) ^ (r & 15);
-        if ((lane & (16 / GPB - 1)) == 0) xsum[(slot * GPB + c / (16 / GPB)) * kSumRows + r] = -136.0f * s;
+        if ((lane & (16 / GPB - 1)) == 0) xsum[(slot * GPB + c / (16 / GPB)) * kSumRows + r] = s;
       }
     }
   }
@@ -303,7 +304,7 @@ struct RowsBody {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int n = 0; n < NT; ++n) q4_pin(acc[m][n]);
+      for (int n = 0; n < NT; ++n) pin(acc[m][n]);
   }
 
   // Step d of a set of D, in slot d: once the next step's rows are here, their
@@ -327,13 +328,13 @@ struct RowsBody {
           s[n][w] = (uint32_t)__builtin_amdgcn_ds_bpermute((16 * d + fr) * 4, (int)sset[n][w]);
       products(cw[d], s, d);
     }
-    q4_lds_barrier();
+    lds_barrier();
     if constexpr (kLoad) next(d, cw[d]);
     __builtin_amdgcn_sched_barrier(0);
   }
-  // D steps, the first at tile kb of its segment.
+  // D steps, `left` of all the steps from the first of them on.
   template <bool kLoad>
-  __device__ __forceinline__ void set(int kb) {
+  __device__ __forceinline__ void set(int left) {
     uint32_t scur[NT][SW];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -341,9 +342,9 @@ struct RowsBody {
       for (int w = 0; w < SW; ++w) scur[n][w] = snext[n][w];
     if constexpr (kLoad) next_scales();
     step<0, kLoad>(scur, true);
-    step<1, kLoad>(scur, kb + 1 < a.KB);
-    step<2, kLoad>(scur, kb + 2 < a.KB);
-    step<3, kLoad>(scur, kb + 3 < a.KB);
+    step<1, kLoad>(scur, kLoad || left > 1);
+    step<2, kLoad>(scur, kLoad || left > 2);
+    step<3, kLoad>(scur, kLoad || left > 3);
   }
   __device__ __forceinline__ void sums() {
     static_assert(D == 4, "set() and the scales' lane groups");
@@ -354,14 +355,10 @@ struct RowsBody {
     next(3, cw[3]);
     q4_arrived<NT + (D - 1) * (kCopies + NT)>();
     sum_rows(0);
-    q4_lds_barrier();
-    const int sets = a.segments * (KBp / D);
-    int kb = 0;
-    for (int i = 0; i + 1 < sets; ++i) {
-      set<true>(kb);
-      kb = kb + D == KBp ? 0 : kb + D;
-    }
-    set<false>(kb);
+    lds_barrier();
+    int left = a.segments * a.KB;  // a set may pass from one segment to the next
+    for (; left > D; left -= D) set<true>(left);
+    set<false>(left);
     __syncthreads();  // the slots are used again; no copy is in flight
   }
 
@@ -445,7 +442,7 @@ struct RowsBody {
 };
 
 template <typename XT, int FMT, int GPB, bool W13>
-__global__ __launch_bounds__(kQrWaves * 64, 4) void q4_rows(Q4Rows a) {  // two workgroups per CU
+__global__ __launch_bounds__(kQrWaves * 64, sizeof(XT) == 2 ? 4 : 2) void q4_rows(Q4Rows a) {  // two workgroups per CU
   constexpr int kMaxMT = sizeof(XT) == 2 ? 3 : 2;
   __shared__ __attribute__((aligned(1024))) char abuf[kQrLds];
   __shared__ __attribute__((aligned(16))) float xsum[4 * GPB * 64];

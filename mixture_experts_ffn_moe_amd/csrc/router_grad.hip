@@ -42,6 +42,17 @@ __device__ __forceinline__ float row16_max(float v) {
   return row16_reduce(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
+// e^x for x <= 0, to 2 units in the last place: 2^(x log2 e) with the product's
+// rest as a first-order term.  0 below -87, where the result is subnormal; NaN
+// stays NaN.  (Against expf, balance loss and gradient at T = 65535: 25 against 27 us.)
+__device__ __forceinline__ float exp_nonpos(float x) {
+  const float hi = 0x1.715476p+0f, lo = 0x1.4ae0bep-26f, ln2 = 0x1.62e430p-1f;  // hi + lo = log2 e
+  const float t = x * hi;
+  const float rest = fmaf(x, lo, fmaf(x, hi, -t));
+  const float r = __builtin_amdgcn_exp2f(t);
+  return x < -87.0f ? 0.0f : fmaf(r, rest * ln2, r);
+}
+
 // Probabilities of the token whose logits start at `row`, 0 past E and for a
 // row that is not `ok` (its values are loaded from a valid address and dropped).
 __device__ __forceinline__ void softmax16(const float (&v)[kPer], int l, int E, bool ok, float (&p)[kPer]) {
@@ -53,7 +64,7 @@ __device__ __forceinline__ void softmax16(const float (&v)[kPer], int l, int E, 
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    p[i] = l + 16 * i < E ? expf(v[i] - m) : 0.0f;
+    p[i] = l + 16 * i < E ? exp_nonpos(v[i] - m) : 0.0f;
     s += p[i];
   }
   s = row16_sum(s);
@@ -668,12 +679,6 @@ __global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
         for (int c = 0; c < 4; ++c) acc[m][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, bx[c], acc[m][c], 0, 0, 0);
       }
   };
-  auto barrier = [] {  // orders LDS accesses, leaves loads in flight
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-  };
-
   // Step s: its x and cut d_logits are here; the next step's d_logits are cut
   // meanwhile.  x is asked for two steps ahead, d_logits three.  (x four steps
   // ahead, in twice the registers: 85 against 81 us at 32767 tokens, 21 against
@@ -692,14 +697,14 @@ __global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
     __builtin_amdgcn_sched_barrier(0);
     cut_d(dr[0], 0);
     load_d(at(2), dr[0]);
-    barrier();
+    lds_barrier();
     auto step = [&](int s, Rows& cur, Cut& d) {
       products(cur, s & 1);
       if (s + 1 < steps) cut_d(d, (s + 1) & 1);
       load_d(at(s + 3), d);  // first: loads return in order, and these are waited for first
       load_x(at(s + 2), cur);
       __builtin_amdgcn_sched_barrier(0);
-      barrier();
+      lds_barrier();
     };
     for (int s = 0; s < steps; s += 2) {
       step(s, xr[0], dr[1]);

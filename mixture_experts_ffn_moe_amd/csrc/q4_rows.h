@@ -2,7 +2,8 @@
 // with SwiGLU and for the down product.
 //
 // A workgroup of 8 waves takes up to 48 rows of one expert (16 MT, MT the
-// fewest 16-row tiles that hold them) and 256 weight rows, a wave 32 of them.
+// fewest 16-row tiles that hold them; fp32 32) and 256 weight rows, a wave 32 of
+// them (fp32 half as many).
 // The codes are the bulk of the bytes and each is used once per row block, so
 // they go from HBM straight to registers in operand order (a wave loads whole
 // 1 KB tiles, 16 bytes a lane), four steps of 128 columns ahead of their use.
@@ -80,8 +81,14 @@ __device__ __forceinline__ RowBlock find_block(const int32_t* __restrict__ offse
 
 }  // namespace
 
-constexpr int kQrTiles = 2;         // weight row tiles of a wave
-constexpr int kQrColTiles = kQrWaves * kQrTiles;
+// Weight row tiles of a wave.  fp32 is bound by its matrix instructions, not by
+// the codes: one tile spreads them over more workgroups and needs no spills (37
+// tokens of H = 448, seven experts of two shards of 160: 15 + 14 against 25 + 23
+// us; 1024 tokens, H = 1024, Im = 512, E = 16, k = 4: 108 + 56 against 133 + 69 us).
+template <typename XT>
+constexpr int kQrTiles = sizeof(XT) == 2 ? 2 : 1;
+template <typename XT>
+constexpr int kQrColTiles = kQrWaves * kQrTiles<XT>;
 constexpr int kQrLds = 65536;       // bytes of the staged rows' slots, at most
 
 // One direct-to-LDS load of 16 bytes a lane from a 64-bit address (rows whose
@@ -106,7 +113,7 @@ __device__ __forceinline__ void q4_arrived() {
 template <typename XT, int FMT, int GPB, int MT, bool W13>
 struct RowsBody {
   static constexpr bool kBf16 = sizeof(XT) == 2;
-  static constexpr int NT = kQrTiles;
+  static constexpr int NT = kQrTiles<XT>;
   static constexpr int MR = 16 * MT;
   static constexpr int D = 4;                          // steps in flight, and of one set of scales
   static constexpr int kRowBytes = kQ4TileK * (int)sizeof(XT);
@@ -398,7 +405,7 @@ struct RowsBody {
     } else {
       // block-scaled half y: the workgroup's columns are one block of 256
       // (repeated tiles past H repeat a stored column: the maximum is unchanged)
-      static_assert(kQrColTiles * 16 == kYBlock, "one y block per workgroup");
+      static_assert(kQrColTiles<XT> * 16 == kYBlock, "one y block per workgroup");
       float* rowmax = reinterpret_cast<float*>(abuf);  // [wave][row]
 #pragma unroll
       for (int m = 0; m < MT; ++m)
@@ -442,11 +449,11 @@ struct RowsBody {
 };
 
 template <typename XT, int FMT, int GPB, bool W13>
-__global__ __launch_bounds__(kQrWaves * 64, sizeof(XT) == 2 ? 4 : 2) void q4_rows(Q4Rows a) {  // two workgroups per CU
+__global__ __launch_bounds__(kQrWaves * 64, 4) void q4_rows(Q4Rows a) {  // two workgroups per CU
   constexpr int kMaxMT = sizeof(XT) == 2 ? 3 : 2;
   __shared__ __attribute__((aligned(1024))) char abuf[kQrLds];
   __shared__ __attribute__((aligned(16))) float xsum[4 * GPB * 64];
-  const int cols = (a.tiles + kQrColTiles - 1) / kQrColTiles;  // workgroups across the output
+  const int cols = (a.tiles + kQrColTiles<XT> - 1) / kQrColTiles<XT>;  // workgroups across the output
   const int col_wg = blockIdx.x % cols;
   const RowBlock blk = find_block<16 * kMaxMT>(a.offsets, a.E, blockIdx.x / cols);
   if (blk.e < 0) return;
@@ -466,7 +473,7 @@ template <typename XT, bool W13>
 inline hipError_t launch_rows_of(const Shape& s, const Q4& q, const Q4Rows& a, hipStream_t st) {
   constexpr int kRows = sizeof(XT) == 2 ? 48 : 32;
   const long long blocks = s.R() / kRows + (s.R() < s.E ? s.R() : s.E);
-  const dim3 grid((unsigned)(blocks * ((a.tiles + kQrColTiles - 1) / kQrColTiles))), block(kQrWaves * 64);
+  const dim3 grid((unsigned)(blocks * ((a.tiles + kQrColTiles<XT> - 1) / kQrColTiles<XT>))), block(kQrWaves * 64);
 #define Q4_GO(FMT, GPB) hipLaunchKernelGGL((q4_rows<XT, FMT, GPB, W13>), grid, block, 0, st, a)
   if (q.format == kQ4Int) {
     if (q.group == 128) Q4_GO(kQ4Int, 1);

@@ -523,12 +523,15 @@ __global__ __launch_bounds__(kWgWaves * 64) void router_weight_grad(
 // d_logits of a step are cut once per workgroup, by all of its threads, and
 // passed through LDS in operand order, one step ahead.  (Cut by every wave
 // for itself, the vector instructions took most of the time: 183 against 81 us
-// at 32767 tokens.)  x wants a lane to hold 8 tokens of one column and lies in
+// at 32767 tokens when that was changed.)  x wants a lane to hold 8 tokens of one column and lies in
 // memory token by token: a lane loads four neighbouring columns of its 8
 // tokens and puts pairs of tokens together with byte permutations; column tile
 // c then holds columns 4 (lane%16) + c.
-// Few column groups mean few partial sums (a workgroup writes 64 experts x its
-// columns), many of them that d_logits are cut and read less often.
+// Small CG means few partial sums (a workgroup writes 64 experts x its columns),
+// large CG that d_logits are cut and read less often.  CG = 2 against 4, both
+// launches: 20 against 24 us at 4096 tokens, 90 against 83 at 32767 (268 MB of x
+// at 3.5 TB/s: bound by the chain of a step, load to cut to product, with two
+// waves a SIMD).
 constexpr int kWbWaves = 8;
 constexpr int kWbTok = 32;  // tokens of a wave's step
 
@@ -563,39 +566,33 @@ __global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
   const int h0 = min(hc, H / kWgCols - 1) * kWgCols;
   const int t_begin = split * per_split, t_end = min(T, t_begin + per_split);
 
-  // byte i not 0: token tb + i counts (the tokens of a whole block are all
-  // below t_end).  Kept as loaded: decoding waits for the load.
-  auto valid = [&](int tb, bool whole) -> uint2 {
-    uint2 ok = make_uint2(0x01010101u, 0x01010101u);
-    if (whole) {
-      if constexpr (MASK) ok = *reinterpret_cast<const uint2*>(mask + tb);  // tb % 8 == 0
-    } else {
-      uint32_t b[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) b[i] = tb + i < t_end && (!MASK || mask[min(tb + i, T - 1)] != 0) ? 1u : 0u;
-      ok = make_uint2(b[0] | b[1] << 8 | b[2] << 16 | b[3] << 24, b[4] | b[5] << 8 | b[6] << 16 | b[7] << 24);
-    }
-    return ok;
+  // Loads are bounded by the hardware and never conditional: rows from t_end on
+  // return zeros without touching memory.  (With branches for the last tokens the
+  // compiler waits for every load in flight before it uses one: 87 against 77 us
+  // at 32767 tokens, 20 against 16 at 4096.)
+  // n tokens from t on, rows of `bytes`: their resource.
+  auto tokens = [&](const void* p, size_t bytes, int t, int n) {
+    const char* at = uniform_ptr((const char*)p + (size_t)min(t, T) * bytes);
+    const uint32_t size = (uint32_t)((size_t)max(0, min(t_end - t, n)) * bytes);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(at), 0, __builtin_amdgcn_readfirstlane((int)size), 0x00020000);
   };
-  auto counts = [](const uint2& ok, int i) { return ((i < 4 ? ok.x : ok.y) >> (8 * (i & 3)) & 0xffu) != 0; };
 
   // d_logits of a step: thread (wave, lane) takes expert `lane` of the tokens
-  // 8 (wave + 8 j) .. + 7
+  // 8 (wave + 8 j) .. + 7; experts past E lie out of bounds too
   struct Cut {
     float v[kPieces][8];
-    uint2 ok[kPieces];
+    uint8_t ok[kPieces];  // of token lane % 8, as loaded: decoding waits for the load
   };
+  const uint32_t d_off = lane < E ? lane * 4u : 0x7ffff000u;
   auto load_d = [&](int t0, Cut& b) {
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
       const int tb = t0 + 8 * (wave + kWbWaves * j);
-      const bool whole = tb + 8 <= t_end;
-      b.ok[j] = valid(tb, whole);
+      if constexpr (MASK) b.ok[j] = mask[min(tb + (lane & 7), T - 1)];
+      const auto rows = tokens(dl, (size_t)E * 4, tb, 8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float* row = dl + (size_t)min(tb + i, T - 1) * E;
-        b.v[j][i] = row[(uint32_t)min(lane, E - 1)];
-      }
+      for (int i = 0; i < 8; ++i)
+        b.v[j][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rows, d_off + (uint32_t)(i * E) * 4u, 0, 0));
     }
   };
   float bsum = 0.0f;
@@ -603,10 +600,11 @@ __global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
 #pragma unroll
     for (int j = 0; j < kPieces; ++j) {
       const int pc = wave + kWbWaves * j;
+      const uint32_t ok = MASK ? (uint32_t)__ballot(b.ok[j] != 0) : ~0u;
       float v[8], r1[8], r2[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        v[i] = lane < E && counts(b.ok[j], i) ? b.v[j][i] : 0.0f;
+        v[i] = (ok >> i & 1) != 0 ? b.v[j][i] : 0.0f;
         bsum += v[i];
         r1[i] = v[i] - __uint_as_float(__float_as_uint(v[i]) & 0xffff0000u);
         r2[i] = r1[i] - __uint_as_float(__float_as_uint(r1[i]) & 0xffff0000u);
@@ -623,23 +621,21 @@ __global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
       *reinterpret_cast<uint4*>(at + 8192) = pack8(r2);
     }
   };
-  // x of this wave's tokens of a step: a uniform row plus the lane's offset
+  // x of this wave's tokens of a step
   struct Rows {
-    uint2 v[8], ok;
+    uint2 v[8];
+    uint8_t ok;  // of token lane % 32
   };
+  const uint32_t x_off = ((uint32_t)(8 * g) * (uint32_t)H + (uint32_t)(h0 + 4 * l)) * 2u;
   auto load_x = [&](int t0, Rows& b) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     const int tw = t0 + tg * kWbTok;
-    const bool whole = tw + kWbTok <= t_end;
-    b.ok = valid(tw + 8 * g, whole);
-    if (whole) {
-      const uint32_t off = ((uint32_t)(8 * g) * (uint32_t)H + (uint32_t)(h0 + 4 * l)) * 2u;
+    if constexpr (MASK) b.ok = mask[min(tw + (lane & 31), T - 1)];
+    const auto rows = tokens(x, (size_t)H * 2, tw, kWbTok);
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        b.v[i] = *reinterpret_cast<const uint2*>((const char*)(x + (size_t)(tw + i) * H) + off);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)  // tokens past the end are dropped below
-        b.v[i] = *reinterpret_cast<const uint2*>(x + (size_t)min(tw + 8 * g + i, T - 1) * H + h0 + 4 * l);
+    for (int i = 0; i < 8; ++i) {
+      const u32x2 v = __builtin_amdgcn_raw_buffer_load_b64(rows, x_off + (uint32_t)i * (uint32_t)H * 2u, 0, 0);
+      b.v[i] = make_uint2(v.x, v.y);
     }
   };
 
@@ -650,14 +646,15 @@ __global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
     for (int c = 0; c < 4; ++c) acc[m][c] = f32x4v{0.f, 0.f, 0.f, 0.f};
 
   auto products = [&](Rows& b, int buf) {
-    bool all = true;
+    if constexpr (MASK) {
+      const uint32_t bits = (uint32_t)__ballot(b.ok != 0);
+      if (bits != ~0u) {  // rows that do not count may hold anything
+        const uint32_t mine = bits >> (8 * g);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) all = all && counts(b.ok, i);
-    if (__any(!all)) {  // rows that do not count may hold anything
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool ok = counts(b.ok, i);
-        b.v[i] = make_uint2(ok ? b.v[i].x : 0u, ok ? b.v[i].y : 0u);
+        for (int i = 0; i < 8; ++i) {
+          const bool ok = (mine >> i & 1) != 0;
+          b.v[i] = make_uint2(ok ? b.v[i].x : 0u, ok ? b.v[i].y : 0u);
+        }
       }
     }
     bf16x8 bx[4];  // column tile c
@@ -681,15 +678,13 @@ __global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
   };
   // Step s: its x and cut d_logits are here; the next step's d_logits are cut
   // meanwhile.  x is asked for two steps ahead, d_logits three.  (x four steps
-  // ahead, in twice the registers: 85 against 81 us at 32767 tokens, 21 against
-  // 19 at 4096.)
+  // ahead, in twice the registers: 73 against 76 us at 32767 tokens, 19 against
+  // 16 at 4096.)
   const int steps = t_end > t_begin ? (t_end - t_begin + kStep - 1) / kStep : 0;
   if (steps > 0) {
     Rows xr[2];
     Cut dr[2];
-    // past the last step: its last tokens again, not used (loads under a
-    // condition would be waited for one by one)
-    auto at = [&](int s) { return min(t_begin + s * kStep, (t_end - 1) / 8 * 8); };
+    auto at = [&](int s) { return t_begin + s * kStep; };  // past the last step: nothing is loaded
     load_d(at(0), dr[0]);
     load_d(at(1), dr[1]);
     load_x(at(0), xr[0]);
@@ -700,15 +695,15 @@ __global__ __launch_bounds__(kWbWaves * 64) void router_weight_grad_bf16(
     lds_barrier();
     auto step = [&](int s, Rows& cur, Cut& d) {
       products(cur, s & 1);
-      if (s + 1 < steps) cut_d(d, (s + 1) & 1);
+      cut_d(d, (s + 1) & 1);  // past the last step: zeros
       load_d(at(s + 3), d);  // first: loads return in order, and these are waited for first
       load_x(at(s + 2), cur);
       __builtin_amdgcn_sched_barrier(0);
       lds_barrier();
     };
-    for (int s = 0; s < steps; s += 2) {
+    for (int s = 0; s < steps; s += 2) {  // one step of zeros more if they are odd
       step(s, xr[0], dr[1]);
-      if (s + 1 < steps) step(s + 1, xr[1], dr[0]);
+      step(s + 1, xr[1], dr[0]);
     }
   }
 

@@ -40,8 +40,8 @@
  * Envelope, beside moe_mi355x.h's: group divides H and Im; otherwise
  * MOE_ERR_UNSUPPORTED.  An unknown format or a group that is not 32, 64 or
  * 128 is MOE_ERR_INVALID_ARG.  Any number of tokens runs; the kernels are
- * built for few rows per expert (up to about 64), where the weights' bytes
- * count.  x and h must be finite and below 2^100 in magnitude (the INT4 codes
+ * built for few rows per expert (blocks of up to 48 share one read of the
+ * codes), where the weights' bytes count.  x and h must be finite and below 2^100 in magnitude (the INT4 codes
  * enter the matrix pipe as 128 + code, and 136 times the operand's sum is
  * taken off again in fp32).
  */

@@ -88,7 +88,9 @@ moe_status moe_router_weight_grad(const moe_shape* shape, const void* x, const f
  * respect to topk_w:
  *   d_topk_w[t, j] = sum_n d_out[t, n] * y[inv[t*k + j], n]
  * y [R, H] as moe_grouped_gemm_down (or moe_q4_down) wrote it, inv
- * moe_permute's (values in [0, R), used unchecked), d_out [T, H] dtype.
+ * moe_permute's (values in [0, R), used unchecked), d_out [T, H] dtype.  The
+ * small-token path of moe_forward and moe_forward_q4 leaves no y in the
+ * workspace: run the down product on the workspace's h and offsets first.
  * Output d_topk_w [T, k] fp32; sums in fp32.  T == 0 enqueues nothing. */
 moe_status moe_finalize_backward(const moe_shape* shape, const void* y, const int32_t* inv,
                                  const void* d_out, float* d_topk_w, void* stream);

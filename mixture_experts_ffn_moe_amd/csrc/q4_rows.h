@@ -21,6 +21,14 @@
 // lines than the L1 holds: 168 against 144 us for the gate|up product at 256
 // tokens, two micro-shards.)
 //
+// Bound: 256 tokens of the layer H = 4096, E = 64, k = 8, two micro-shards of 768,
+// INT4, group 64: the gate|up product takes 132 us for 430 MB (3.3 TB/s), the down
+// product 75 us for 215 MB; without its products the first takes 95 - 112 us,
+// with its codes from the L2 128 us.  What bounds it is the length of a step in a
+// wave (operands from LDS, conversion, products, scales) at 16 waves a CU, which
+// 128 registers a lane allow.  Tried and not kept: row sums behind the products,
+// workgroups of one expert on one XCD.
+//
 // INT4 codes enter as 128 + code (q4.h).  The 136 * sum(x) too much of a
 // group is the same for every weight row: each wave sums the chunks that it
 // copied itself (8 values on the two-element dot product, then over the group's

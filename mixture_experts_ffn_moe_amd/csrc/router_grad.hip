@@ -77,7 +77,9 @@ __device__ __forceinline__ void softmax16(const float (&v)[kPer], int l, int E, 
 // Balance loss.  One workgroup of 16 waves takes 64 tokens a step and a
 // contiguous run of tokens in all; its sums go to the workspace in fp64, and
 // a second launch of one workgroup adds them (one workgroup alone finishes by
-// itself).
+// itself).  T = 4096, E = 64, k = 8: 5.0 + 2.8 us, launches; T = 65535: 8.2 + 5.1
+// us for 19 MB of logits and ids, the vector instructions of the softmax and two
+// launches.
 constexpr int kBalWaves = 16;
 constexpr int kBalStep = kBalWaves * kTokWave;  // tokens per step of a workgroup
 constexpr int kBalBlocks = 256;                 // at most one workgroup per CU
@@ -217,7 +219,8 @@ __global__ __launch_bounds__(kBalWaves * 64) void balance_finish(const BalancePa
 // ---------------------------------------------------------------------------
 // Gradient of the logits: 16 lanes per token as above.  The routes' values
 // are scattered to the experts through an LDS row per token (written and read
-// by the token's own wave).
+// by the token's own wave).  T = 4096, E = 64, k = 8: 4.3 us; T = 65535: 11.6 us
+// for 40 MB (3.4 TB/s).
 constexpr int kRbWaves = 4;
 
 __global__ __launch_bounds__(kRbWaves * 64) void route_backward(
@@ -306,7 +309,8 @@ __global__ __launch_bounds__(kRbWaves * 64) void route_backward(
 // ---------------------------------------------------------------------------
 // Gradient of the routing weights: one workgroup per token, as the finalize
 // whose backward pass it is; d_out's row is read once per eight routes, each
-// thread taking 8 columns (one y block) of d_out and of eight rows of y.
+// thread taking 8 columns (inside one y block) of d_out and of eight rows of y.
+// Bound by HBM: T = 4096, H = 4096, k = 8, bf16: 302 MB in 54 us (5.6 TB/s).
 constexpr int kFbThreads = 256;
 constexpr int kFbRoutes = 8;
 
@@ -410,7 +414,8 @@ __global__ __launch_bounds__(kFbThreads) void finalize_backward(const YT* __rest
 // holds columns q, q + 4, ..., and a lane's four results of a row are
 // neighbours again.  A workgroup covers 64 experts x 64 columns over one run
 // of tokens, its 16 waves taking every 16th step of 4 tokens; the waves' sums
-// are added through LDS in a fixed order.
+// are added through LDS in a fixed order.  T = 4096, H = 4096: 42 us for 67 MB, the
+// matrix instructions 14 of them.
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 constexpr int kWgWaves = 16;
 constexpr int kWgCols = 64;

@@ -96,7 +96,10 @@ moe_status moe_q4_down(const moe_shape* shape, const moe_q4_spec* q4, const void
  * H % 2048 == 0, T rounded up to 4 times H and T times mu times Im rounded up
  * to 128 both <= 65536) takes a path of its own, as in moe_forward: routing is
  * the same bits as the step-wise path, the output matches it within rounding
- * (sums in another order, y never stored). */
+ * (sums in another order, y never stored).  Up to 1024 tokens of other bf16
+ * batches the router's fp64 sums run in another order than moe_route's: a logit
+ * can differ by its last fp32 bit only where its sum lies within the order's
+ * difference (about 2^-40 of the terms' magnitudes) of a rounding border. */
 moe_status moe_forward_q4(const moe_shape* shape, const moe_q4_spec* q4, const void* x,
                           const float* wg, const float* bias, const void* w1_codes,
                           const void* w1_scales, const void* w2_codes, const void* w2_scales,

@@ -370,9 +370,11 @@ def moe_forward_shared(shape, Is, x, wg, bias, w1, w2, w1s, w2s, out, workspace,
            "moe_forward_shared")
 
 
-def _on_current(*tensors):
-    """The library launches on the current device: every (GPU) tensor has to be on it."""
+def _on_current(*tensors, stream=None):
+    """The library launches on the current device: every (GPU) tensor and the stream have to be on it."""
     here = torch.cuda.current_device()
+    if stream is not None and getattr(stream, "device_index", here) != here:
+        raise ValueError(f"the stream is on cuda:{stream.device_index}, the current device is cuda:{here}")
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
@@ -398,7 +400,7 @@ def moe_q4_quantize_w13(shape, q4, w1, codes, scales, stream=None):
     z = moe_q4_get_sizes(shape, q4)
     args = (_arg("w1", w1, _layer_dtype(shape), shape.micro_count * shape.E * 2 * shape.Im * shape.H),
             _arg_bytes("codes", codes, z["w1_codes"]), _arg_bytes("scales", scales, z["w1_scales"]))
-    _on_current(w1, codes, scales)
+    _on_current(w1, codes, scales, stream=stream)
     _check(lib.moe_q4_quantize_w13(ctypes.byref(shape), ctypes.byref(q4), *args, _stream(stream)),
            "moe_q4_quantize_w13")
 
@@ -408,7 +410,7 @@ def moe_q4_quantize_down(shape, q4, w2, codes, scales, stream=None):
     z = moe_q4_get_sizes(shape, q4)
     args = (_arg("w2", w2, _layer_dtype(shape), shape.micro_count * shape.E * shape.H * shape.Im),
             _arg_bytes("codes", codes, z["w2_codes"]), _arg_bytes("scales", scales, z["w2_scales"]))
-    _on_current(w2, codes, scales)
+    _on_current(w2, codes, scales, stream=stream)
     _check(lib.moe_q4_quantize_down(ctypes.byref(shape), ctypes.byref(q4), *args, _stream(stream)),
            "moe_q4_quantize_down")
 
@@ -419,7 +421,7 @@ def moe_q4_w13_swiglu(shape, q4, x, perm, offsets, w1_codes, w1_scales, h, strea
     args = (_arg("x", x, dt, T * H), _arg("perm", perm, torch.int32, R), _arg("offsets", offsets, torch.int32, E + 1),
             _arg_bytes("w1_codes", w1_codes, z["w1_codes"]), _arg_bytes("w1_scales", w1_scales, z["w1_scales"]),
             _arg("h", h, dt, R * shape.micro_count * shape.Im))
-    _on_current(x, perm, offsets, w1_codes, w1_scales, h)
+    _on_current(x, perm, offsets, w1_codes, w1_scales, h, stream=stream)
     _check(lib.moe_q4_w13_swiglu(ctypes.byref(shape), ctypes.byref(q4), *args, _stream(stream)), "moe_q4_w13_swiglu")
 
 
@@ -429,7 +431,7 @@ def moe_q4_down(shape, q4, h, offsets, w2_codes, w2_scales, y, stream=None):
     args = (_arg("h", h, _layer_dtype(shape), R * shape.micro_count * shape.Im),
             _arg("offsets", offsets, torch.int32, E + 1), _arg_bytes("w2_codes", w2_codes, z["w2_codes"]),
             _arg_bytes("w2_scales", w2_scales, z["w2_scales"]), _arg_bytes("y", y, y_nbytes(shape, R)))
-    _on_current(h, offsets, w2_codes, w2_scales, y)
+    _on_current(h, offsets, w2_codes, w2_scales, y, stream=stream)
     _check(lib.moe_q4_down(ctypes.byref(shape), ctypes.byref(q4), *args, _stream(stream)), "moe_q4_down")
 
 
@@ -443,7 +445,7 @@ def moe_forward_q4(shape, q4, x, wg, bias, w1_codes, w1_scales, w2_codes, w2_sca
             _arg_bytes("w2_codes", w2_codes, z["w2_codes"]), _arg_bytes("w2_scales", w2_scales, z["w2_scales"]),
             _arg("out", out, dt, T * H))
     ws, nbytes = _workspace(workspace)
-    _on_current(x, wg, bias, w1_codes, w1_scales, w2_codes, w2_scales, out, workspace)
+    _on_current(x, wg, bias, w1_codes, w1_scales, w2_codes, w2_scales, out, workspace, stream=stream)
     _check(lib.moe_forward_q4(ctypes.byref(shape), ctypes.byref(q4), *args, ws, nbytes, _stream(stream)),
            "moe_forward_q4")
 
@@ -462,7 +464,7 @@ def moe_balance_loss(shape, logits, topk_ids, token_mask, counts, mean_prob, los
             _arg("token_mask", token_mask, torch.uint8, T, nullable=True), _arg("counts", counts, torch.int32, E),
             _arg("mean_prob", mean_prob, torch.float32, E), _arg("loss", loss, torch.float32, 1))
     ws, nbytes = _workspace(workspace)
-    _on_current(logits, topk_ids, token_mask, counts, mean_prob, loss, workspace)
+    _on_current(logits, topk_ids, token_mask, counts, mean_prob, loss, workspace, stream=stream)
     _check(lib.moe_balance_loss(ctypes.byref(shape), *args, ws, nbytes, _stream(stream)), "moe_balance_loss")
 
 
@@ -476,7 +478,7 @@ def moe_route_backward(shape, logits, topk_ids, topk_w, token_mask, counts, d_to
             _arg("d_topk_w", d_topk_w, torch.float32, T * k, nullable=True),
             _arg("d_loss", d_loss, torch.float32, 1, nullable=True),
             _arg("d_logits", d_logits, torch.float32, T * E))
-    _on_current(logits, topk_ids, topk_w, token_mask, counts, d_topk_w, d_loss, d_logits)
+    _on_current(logits, topk_ids, topk_w, token_mask, counts, d_topk_w, d_loss, d_logits, stream=stream)
     _check(lib.moe_route_backward(ctypes.byref(shape), *args, _stream(stream)), "moe_route_backward")
 
 
@@ -491,7 +493,7 @@ def moe_router_weight_grad(shape, x, d_logits, token_mask, d_wg, d_bias, workspa
             _arg("token_mask", token_mask, torch.uint8, T, nullable=True),
             _arg("d_wg", d_wg, torch.float32, E * H), _arg("d_bias", d_bias, torch.float32, E, nullable=True))
     ws, nbytes = _workspace(workspace)
-    _on_current(x, d_logits, token_mask, d_wg, d_bias, workspace)
+    _on_current(x, d_logits, token_mask, d_wg, d_bias, workspace, stream=stream)
     _check(lib.moe_router_weight_grad(ctypes.byref(shape), *args, ws, nbytes, _stream(stream)),
            "moe_router_weight_grad")
 
@@ -502,7 +504,7 @@ def moe_finalize_backward(shape, y, inv, d_out, d_topk_w, stream=None):
     R = T * k
     args = (_arg_bytes("y", y, y_nbytes(shape, R)), _arg("inv", inv, torch.int32, R),
             _arg("d_out", d_out, _layer_dtype(shape), T * H), _arg("d_topk_w", d_topk_w, torch.float32, R))
-    _on_current(y, inv, d_out, d_topk_w)
+    _on_current(y, inv, d_out, d_topk_w, stream=stream)
     _check(lib.moe_finalize_backward(ctypes.byref(shape), *args, _stream(stream)), "moe_finalize_backward")
 
 

@@ -27,7 +27,7 @@
 // with its codes from the L2 128 us.  What bounds it is the length of a step in a
 // wave (operands from LDS, conversion, products, scales) at 16 waves a CU, which
 // 128 registers a lane allow.  Tried and not kept: row sums behind the products,
-// workgroups of one expert on one XCD.
+// workgroups of one expert on one XCD, halved workgroups in the last round.
 //
 // INT4 codes enter as 128 + code (q4.h).  The 136 * sum(x) too much of a
 // group is the same for every weight row: each wave sums the chunks that it

@@ -50,14 +50,6 @@ __device__ __forceinline__ void wait_vmcnt() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-// A barrier that orders LDS accesses and leaves loads in flight (the one of
-// __syncthreads waits for them).
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
 // One direct-to-LDS load: every lane copies 16 bytes from sbase + voff (bytes)
 // to LDS address lds + 16 * lane.  Issued as inline asm so the compiler's
 // wait-count tracking does not serialise the pipeline: callers wait on vmcnt

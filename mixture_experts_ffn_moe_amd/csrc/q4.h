@@ -2,6 +2,7 @@
 // conversion and the internal launchers (storage and semantics: moe_q4.h).
 #pragma once
 
+#include "lds_barrier.h"
 #include "moe_common.h"
 
 namespace moe {

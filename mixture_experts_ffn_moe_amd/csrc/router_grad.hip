@@ -7,6 +7,7 @@
 // no result depends on the order of atomics.
 #include "../../include/moe_router_grad.h"
 #include "api_check.h"
+#include "lds_barrier.h"
 
 #include <algorithm>
 

@@ -15,6 +15,7 @@
 // result is bitwise reproducible.  One workgroup per token; each thread moves
 // 16-byte vectors, so every row read is fully coalesced.
 #include "moe_common.h"
+#include "row_grid.h"
 
 namespace moe {
 namespace {
@@ -47,10 +48,11 @@ __global__ __launch_bounds__(256) void finalize_kernel(const YT* __restrict__ y,
                                                        const int32_t* __restrict__ inv,
                                                        const float* __restrict__ w,
                                                        const YT* __restrict__ ys,
-                                                       const int8_t* __restrict__ yse, int H, int k,
-                                                       T* __restrict__ out) {
+                                                       const int8_t* __restrict__ yse, int tokens, int H,
+                                                       int k, T* __restrict__ out) {
   constexpr int V = 8;  // columns per thread
-  const int t = blockIdx.x;
+  const int t = grid_row();
+  if (t >= tokens) return;
   const int32_t* rows = inv + (size_t)t * k;
   const float* wt = w + (size_t)t * k;
   for (int c = threadIdx.x * V; c < H; c += blockDim.x * V) {
@@ -101,12 +103,12 @@ hipError_t launch_finalize(const Shape& s, const void* y, const int32_t* inv, co
     // block-scaled half: the exponent plane follows the values plane
     const int8_t* ye = (const int8_t*)y + (size_t)s.R() * s.H * 2;
     const int8_t* yse = ys ? (const int8_t*)ys + (size_t)s.T * s.H * 2 : nullptr;
-    hipLaunchKernelGGL((finalize_kernel<uint16_t, _Float16>), dim3(s.T), dim3(256), 0, st,
-                       (const _Float16*)y, ye, inv, w, (const _Float16*)ys, yse, s.H, s.k,
+    hipLaunchKernelGGL((finalize_kernel<uint16_t, _Float16>), row_grid(s.T), dim3(256), 0, st,
+                       (const _Float16*)y, ye, inv, w, (const _Float16*)ys, yse, s.T, s.H, s.k,
                        (uint16_t*)out);
   } else {
-    hipLaunchKernelGGL((finalize_kernel<float, float>), dim3(s.T), dim3(256), 0, st, (const float*)y,
-                       (const int8_t*)nullptr, inv, w, (const float*)ys, (const int8_t*)nullptr, s.H,
+    hipLaunchKernelGGL((finalize_kernel<float, float>), row_grid(s.T), dim3(256), 0, st, (const float*)y,
+                       (const int8_t*)nullptr, inv, w, (const float*)ys, (const int8_t*)nullptr, s.T, s.H,
                        s.k, (float*)out);
   }
   return hipGetLastError();

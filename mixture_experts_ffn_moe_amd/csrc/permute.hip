@@ -21,6 +21,7 @@
 // no atomics, so perm and inv are deterministic; every workgroup computes the
 // same counts and offsets and workgroup 0 writes them.
 #include "moe_common.h"
+#include "row_grid.h"
 
 #include <algorithm>
 
@@ -182,9 +183,10 @@ __global__ __launch_bounds__(kWaves * kWave) void permute_hist_kernel(
 
 template <typename T>
 __global__ __launch_bounds__(256) void gather_kernel(const T* __restrict__ x,
-                                                     const int32_t* __restrict__ perm, int H,
-                                                     int k, T* __restrict__ xp) {
-  const int p = blockIdx.x;
+                                                     const int32_t* __restrict__ perm, int R,
+                                                     int H, int k, T* __restrict__ xp) {
+  const int p = grid_row();
+  if (p >= R) return;
   const int t = perm[p] / k;
   constexpr int V = 16 / sizeof(T);
   const uint4* src = reinterpret_cast<const uint4*>(x + (size_t)t * H);
@@ -233,13 +235,13 @@ hipError_t launch_permute_hist(const Shape& s, const int32_t* ids, const int32_t
 
 hipError_t launch_gather(const Shape& s, const void* x, const int32_t* perm, void* xp,
                          hipStream_t st) {
-  const unsigned R = (unsigned)s.R();
+  const int R = (int)s.R();
   if (s.bf16)
-    hipLaunchKernelGGL(gather_kernel<uint16_t>, dim3(R), dim3(256), 0, st, (const uint16_t*)x,
-                       perm, s.H, s.k, (uint16_t*)xp);
+    hipLaunchKernelGGL(gather_kernel<uint16_t>, row_grid(R), dim3(256), 0, st, (const uint16_t*)x,
+                       perm, R, s.H, s.k, (uint16_t*)xp);
   else
-    hipLaunchKernelGGL(gather_kernel<float>, dim3(R), dim3(256), 0, st, (const float*)x, perm,
-                       s.H, s.k, (float*)xp);
+    hipLaunchKernelGGL(gather_kernel<float>, row_grid(R), dim3(256), 0, st, (const float*)x, perm,
+                       R, s.H, s.k, (float*)xp);
   return hipGetLastError();
 }
 

@@ -8,6 +8,7 @@
 #include "../../include/moe_router_grad.h"
 #include "api_check.h"
 #include "lds_barrier.h"
+#include "row_grid.h"
 
 #include <algorithm>
 
@@ -387,10 +388,11 @@ template <typename T, typename YT>
 __global__ __launch_bounds__(kFbThreads) void finalize_backward(const YT* __restrict__ y,
                                                                 const int8_t* __restrict__ ye,
                                                                 const int32_t* __restrict__ inv,
-                                                                const T* __restrict__ d_out, int H, int k,
-                                                                float* __restrict__ d_w) {
+                                                                const T* __restrict__ d_out, int tokens, int H,
+                                                                int k, float* __restrict__ d_w) {
   __shared__ float part[kFbThreads / 64][kFbRoutes];
-  const int t = blockIdx.x;
+  const int t = grid_row();
+  if (t >= tokens) return;
   inv += (size_t)t * k;
   d_w += (size_t)t * k;
   d_out += (size_t)t * H;
@@ -929,12 +931,12 @@ moe_status moe_finalize_backward(const moe_shape* shape, const void* y, const in
   MOE_CHECK(check_ptr(y)); MOE_CHECK(check_ptr(inv)); MOE_CHECK(check_ptr(d_out)); MOE_CHECK(check_ptr(d_topk_w));
   hipStream_t st = (hipStream_t)stream;
   if (s.bf16)
-    hipLaunchKernelGGL((moe::finalize_backward<uint16_t, _Float16>), dim3(s.T), dim3(moe::kFbThreads), 0, st,
+    hipLaunchKernelGGL((moe::finalize_backward<uint16_t, _Float16>), moe::row_grid(s.T), dim3(moe::kFbThreads), 0, st,
                        (const _Float16*)y, (const int8_t*)y + (size_t)s.R() * s.H * 2, inv, (const uint16_t*)d_out,
-                       s.H, s.k, d_topk_w);
+                       s.T, s.H, s.k, d_topk_w);
   else
-    hipLaunchKernelGGL((moe::finalize_backward<float, float>), dim3(s.T), dim3(moe::kFbThreads), 0, st,
-                       (const float*)y, (const int8_t*)nullptr, inv, (const float*)d_out, s.H, s.k, d_topk_w);
+    hipLaunchKernelGGL((moe::finalize_backward<float, float>), moe::row_grid(s.T), dim3(moe::kFbThreads), 0, st,
+                       (const float*)y, (const int8_t*)nullptr, inv, (const float*)d_out, s.T, s.H, s.k, d_topk_w);
   return hip_status(hipGetLastError());
 }
 

@@ -62,6 +62,7 @@ moe_status moe_balance_loss(const moe_shape* shape, const float* logits, const i
  *                  w[t,j] * (d_topk_w[t,j] - sum_i w[t,i] d_topk_w[t,i]), else 0
  *   weights part, renormalize = 0:
  *                  p[t,e] * ((d_topk_w[t,j] if e = topk_ids[t,j] else 0) - sum_i w[t,i] d_topk_w[t,i])
+ *   topk_ids and topk_w are read only with d_topk_w, NULL is allowed without it.
  *   counts [E]: moe_balance_loss's for the same ids and mask; read only with
  *   d_loss, NULL is allowed without it.  d_loss [1] fp32 on the device.
  * Output d_logits [T, E] fp32 (every element written). */

@@ -471,8 +471,10 @@ def moe_balance_loss(shape, logits, topk_ids, token_mask, counts, mean_prob, los
 def moe_route_backward(shape, logits, topk_ids, topk_w, token_mask, counts, d_topk_w, d_loss, d_logits, stream=None):
     """Gradient of the router logits from those of the routing weights and of the balance loss (either may be None)."""
     T, E, k = shape.T, shape.E, shape.k
-    args = (_arg("logits", logits, torch.float32, T * E), _arg("topk_ids", topk_ids, torch.int32, T * k),
-            _arg("topk_w", topk_w, torch.float32, T * k),
+    unread = d_topk_w is None
+    args = (_arg("logits", logits, torch.float32, T * E),
+            _arg("topk_ids", topk_ids, torch.int32, T * k, nullable=unread),
+            _arg("topk_w", topk_w, torch.float32, T * k, nullable=unread),
             _arg("token_mask", token_mask, torch.uint8, T, nullable=True),
             _arg("counts", counts, torch.int32, E, nullable=True),
             _arg("d_topk_w", d_topk_w, torch.float32, T * k, nullable=True),

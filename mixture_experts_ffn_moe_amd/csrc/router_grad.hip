@@ -863,10 +863,11 @@ moe_status moe_route_backward(const moe_shape* shape, const float* logits, const
   MOE_CHECK(check_shape(shape, &s));
   if (s.T == 0) return MOE_OK;
   if (d_topk_w == nullptr && d_loss == nullptr) return MOE_ERR_INVALID_ARG;
-  MOE_CHECK(check_ptr(logits)); MOE_CHECK(check_ptr(topk_ids)); MOE_CHECK(check_ptr(topk_w));
-  MOE_CHECK(check_ptr(d_logits));
+  MOE_CHECK(check_ptr(logits)); MOE_CHECK(check_ptr(d_logits));
   if (token_mask != nullptr) MOE_CHECK(check_ptr(token_mask));
-  if (d_topk_w != nullptr) MOE_CHECK(check_ptr(d_topk_w));
+  if (d_topk_w != nullptr) {
+    MOE_CHECK(check_ptr(d_topk_w)); MOE_CHECK(check_ptr(topk_ids)); MOE_CHECK(check_ptr(topk_w));
+  }
   if (d_loss != nullptr) { MOE_CHECK(check_ptr(d_loss)); MOE_CHECK(check_ptr(counts)); }
   const int blocks = std::min(2048, moe::ceil_div(s.T, moe::kRbWaves * moe::kTokWave));
   hipLaunchKernelGGL(moe::route_backward, dim3(blocks), dim3(moe::kRbWaves * 64), 0, (hipStream_t)stream, logits,

@@ -537,15 +537,21 @@ __global__ __launch_bounds__(kWgWaves * 64) void router_weight_grad(
 // c then holds columns 4 (lane%16) + c.
 // Small CG means few partial sums (a workgroup writes 64 experts x its columns),
 // large CG that d_logits are cut and read less often.  CG = 2 against 4, both
-// launches: 20 against 24 us at 4096 tokens, 90 against 83 at 32767 (268 MB of x
-// at 3.5 TB/s: bound by the chain of a step, load to cut to product, with two
-// waves a SIMD).
+// launches with a mask (without one CG = 4 gains a little less), us:
+//   H = 1024: T = 16384 31 / 39, 65536 56 / 61, 98304 79 / 74, 262144 172 / 158
+//   H = 2048: T = 16384 33 / 34, 49152 65 / 64, 131071 157 / 147
+//   H = 4096: T = 4096 21 / 24, 16384 46 / 46, 24576 62 / 60, 65535 152 / 140
+//   H = 8192: T = 4096 29 / 30, 16384 77 / 73, 65535 288 / 261
+// and of narrower x, whose few columns CG = 4 leaves to few waves, H = 64: T =
+// 1572864 186 / 252, H = 256: 393216 104 / 132, H = 512: 196608 87 / 92, 1048576
+// 325 / 307.  Bound by the chain of a step, load to cut to product, with two waves
+// a SIMD (268 MB of x in 71 us: 3.8 TB/s).
 constexpr int kWbWaves = 8;
 constexpr int kWbTok = 32;  // tokens of a wave's step
 
-inline int wgrad_groups(int T) { return T >= 16384 ? 4 : 2; }
+inline int wgrad_groups(int T, int H) { return H >= 512 && (long long)T * H >= 3 << 25 ? 4 : 2; }
 inline int wgrad_bf16_splits(int T, int H) {
-  const int cg = wgrad_groups(T), cols = (H / kWgCols + cg - 1) / cg, step = kWbWaves / cg * kWbTok;
+  const int cg = wgrad_groups(T, H), cols = (H / kWgCols + cg - 1) / cg, step = kWbWaves / cg * kWbTok;
   return std::max(1, std::min(kWgBlocks / cols, (T + 2 * step - 1) / (2 * step)));
 }
 
@@ -903,7 +909,7 @@ moe_status moe_router_weight_grad(const moe_shape* shape, const void* x, const f
   float* part = (float*)workspace;
   float* bpart = part + (size_t)splits * moe::kMaxExperts * s.H;
   if (s.bf16) {
-    const int cg = moe::wgrad_groups(s.T);
+    const int cg = moe::wgrad_groups(s.T, s.H);
     const dim3 grid(moe::ceil_div(s.H / moe::kWgCols, cg), splits);
     per = moe::ceil_div(per, moe::kWbTok) * moe::kWbTok;
 #define MOE_GO(CG, MASK)                                                                                           \

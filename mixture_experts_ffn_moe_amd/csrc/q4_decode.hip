@@ -21,10 +21,17 @@
 // MB, INT4, group 128) takes 5 + 35 + 24 us; the codes arrive at about 5.7 TB/s
 // once a kernel streams, and each launch, the routing finish, the rows' way to
 // LDS and the last sums (about 9 us a kernel) stand before and behind the stream.
+// At T = 16 (groups of 32, E2M1: 5 + 54 + 33 us) the rows of h pass LDS in two
+// rounds, and the codes of the second are asked for only when its rows are.
 // Parts cut in units of four tiles instead of eight: 92 against 92 us at T = 16, 68
 // against 64 at T = 8; not kept.
-// Both keep 8 KB of codes in flight per wave (128 KB a CU) and issue a tile's
-// successor as soon as its registers are free.  The loads are nontemporal (the
+// Both ask for 8 KB of codes a wave ahead (128 KB a CU) and for a tile's
+// successor as soon as its registers are free.  In the down product at groups of
+// 128 the compiler does not keep that up: it widens the ring's eight 16-bit scales
+// together at the end of a pass, behind a wait for every load, so that the ring
+// runs empty every eight tiles (and the first time before the staged rows' own
+// wait).  At groups of 64 and 32, whose scales come in whole words, it waits for a
+// tile's loads alone.  The loads are nontemporal (the
 // layer at T = 8: 64.5 against 67.9 us in the kernel trace, at T = 16 with
 // groups of 32: 92 against 100 us).
 #include "decode_route.h"
@@ -55,7 +62,8 @@ struct Q4DecodeArgs {
 };
 
 // Scales stay as loaded (bf16, two a word): a conversion would wait for the
-// loads where they are issued.
+// loads where they are issued.  (A single one, load_tile_scales<1>, is widened to
+// its word there: see the top.)
 // The scales of four neighbouring tiles (8 GPB bytes, aligned to that).
 template <int GPB>
 __device__ __forceinline__ void load_step_scales(const uint16_t* p, uint32_t (&s)[2 * GPB]) {
@@ -126,8 +134,10 @@ __global__ __launch_bounds__(kDqWaves * 64) void q4_decode_w13(Q4DecodeArgs a) {
   const int Tp = (a.T + 3) & ~3;                // tokens of a row of xsum
   const int chunks = a.T * (a.H / 8);           // 16-byte chunks of the tokens' rows
 
-  // the rows are on their way while the routing's partial sums are read; then
-  // to LDS, chunks XOR-swizzled by the token, and their groups' sums.  64
+  // the rows are on their way while the routing's partial sums are read (INT4; in
+  // the E2M1 instances the compiler keeps xv in private memory, 144 bytes a lane,
+  // and waits for one chunk before it asks for the next: up to eight round
+  // trips at T = 16); then to LDS, chunks XOR-swizzled by the token, and their groups' sums.  64
   // neighbouring chunks are one token's (H / 8 is a multiple of 256).
   uint4 xv[kDqStage];
 #pragma unroll
@@ -201,7 +211,10 @@ __global__ __launch_bounds__(kDqWaves * 64) void q4_decode_w13(Q4DecodeArgs a) {
     if ((i & 3) == 3) load_step_scales<GPB>(sg.sp + (kb + i - 3) * GPB, rsc[i / 4]);
   };
   auto store_h = [&](int e, int col, const f32x4& v) {
-    // tile columns 0-7 gate, 8-15 the up columns of the same 8
+    // tile columns 0-7 gate, 8-15 the up columns of the same 8.  h is rounded to the
+    // layer's type, as the step-wise products and the dense layer do: it is an output
+    // of the workspace, and the down product's operands are bf16.  (With h and y in
+    // fp32 the output would be 0.0017 from the 64-bit result instead of 0.0024.)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const float up = __shfl_xor(v[r], 8);

@@ -22,11 +22,14 @@
 // tokens, two micro-shards.)
 //
 // Bound: 256 tokens of the layer H = 4096, E = 64, k = 8, two micro-shards of 768,
-// INT4, group 64: the gate|up product takes 132 us for 430 MB (3.3 TB/s), the down
-// product 75 us for 215 MB; without its products the first takes 95 - 112 us,
-// with its codes from the L2 128 us.  What bounds it is the length of a step in a
+// INT4, group 64: the gate|up product takes 134 - 140 us for 430 MB (3.1 - 3.2 TB/s),
+// the down product 77 - 81 us for 215 MB; without its products the first takes 95 -
+// 112 us, with its codes from the L2 128 us.  What bounds it is the length of a step in a
 // wave (operands from LDS, conversion, products, scales) at 16 waves a CU, which
-// 128 registers a lane allow.  Tried and not kept: row sums behind the products,
+// 128 registers a lane allow (at groups of 128 the gate|up product spills six of them
+// in INT4 and one in E2M1, at groups of 64 the INT4 down product one, outside the steps).
+// Every block of rows reads and converts all codes of its expert again: past some 1500
+// tokens of this layer (of one or two shards) the dense bf16 layer is the faster one.  Tried and not kept: row sums behind the products,
 // workgroups of one expert on one XCD, halved workgroups in the last round.
 //
 // INT4 codes enter as 128 + code (q4.h).  The 136 * sum(x) too much of a
@@ -381,7 +384,8 @@ struct RowsBody {
   __device__ __forceinline__ int row_of(int m, int r) const { return blk.row0 + 16 * m + 4 * g + r; }
 
   __device__ __forceinline__ void store_h() const {
-    // tile columns 0-7 gate, 8-15 the up columns of the same 8
+    // tile columns 0-7 gate, 8-15 the up columns of the same 8; h in the layer's type,
+    // as the dense product writes it (the down product's operands are bf16 in bf16 layers)
     const int per = a.N / 16;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -411,7 +415,8 @@ struct RowsBody {
               ((float*)a.out)[(size_t)p * a.N + (tile0 + n) * 16 + fr] = acc[m][n][r];
           }
     } else {
-      // block-scaled half y: the workgroup's columns are one block of 256
+      // block-scaled half y, the dense layer's (11 bits in the bytes of bf16, moe_common.h):
+      // the workgroup's columns are one block of 256
       // (repeated tiles past H repeat a stored column: the maximum is unchanged)
       static_assert(kQrColTiles<XT> * 16 == kYBlock, "one y block per workgroup");
       float* rowmax = reinterpret_cast<float*>(abuf);  // [wave][row]

@@ -79,8 +79,8 @@ __device__ __forceinline__ void softmax16(const float (&v)[kPer], int l, int E, 
 // Balance loss.  One workgroup of 16 waves takes 64 tokens a step and a
 // contiguous run of tokens in all; its sums go to the workspace in fp64, and
 // a second launch of one workgroup adds them (one workgroup alone finishes by
-// itself).  T = 4096, E = 64, k = 8: 5.0 + 2.8 us, launches; T = 65535: 8.2 + 5.1
-// us for 19 MB of logits and ids, the vector instructions of the softmax and two
+// itself).  T = 4096, E = 64, k = 8: 5.0 + 2.7 us, launches; T = 65535: 8.0 - 9.5 +
+// 5.0 us for 19 MB of logits and ids, the vector instructions of the softmax and two
 // launches.
 constexpr int kBalWaves = 16;
 constexpr int kBalStep = kBalWaves * kTokWave;  // tokens per step of a workgroup
@@ -312,7 +312,8 @@ __global__ __launch_bounds__(kRbWaves * 64) void route_backward(
 // Gradient of the routing weights: one workgroup per token, as the finalize
 // whose backward pass it is; d_out's row is read once per eight routes, each
 // thread taking 8 columns (inside one y block) of d_out and of eight rows of y.
-// Bound by HBM: T = 4096, H = 4096, k = 8, bf16: 302 MB in 54 us (5.6 TB/s).
+// Bound by HBM: T = 4096, H = 4096, k = 8, bf16: 302 MB in 54 us (5.6 TB/s); fp32,
+// T = 1024: 134 MB in 28 us at k = 8, 67 MB in 15 us at k = 4.
 constexpr int kFbThreads = 256;
 constexpr int kFbRoutes = 8;
 
@@ -350,7 +351,9 @@ __device__ __forceinline__ float ydot8(const _Float16* y, const int8_t* ye, size
 }
 
 // NJ routes [j0, j0 + NJ) of token t (NJ known to the compiler: the NJ row
-// loads of a step are all in flight before the first is used).
+// loads of a step are all in flight before the first is used; of fp32 rows at NJ = 8
+// it takes one row's loads at a time, to which the other workgroups of a CU
+// give cover: 4.8 TB/s, and 4.5 at NJ = 4).
 template <int NJ, typename T, typename YT>
 __device__ __forceinline__ void finalize_backward_routes(const YT* __restrict__ y, const int8_t* __restrict__ ye,
                                                          const int32_t* __restrict__ inv,
@@ -417,8 +420,10 @@ __global__ __launch_bounds__(kFbThreads) void finalize_backward(const YT* __rest
 // holds columns q, q + 4, ..., and a lane's four results of a row are
 // neighbours again.  A workgroup covers 64 experts x 64 columns over one run
 // of tokens, its 16 waves taking every 16th step of 4 tokens; the waves' sums
-// are added through LDS in a fixed order.  T = 4096, H = 4096: 42 us for 67 MB, the
-// matrix instructions 14 of them.
+// are added through LDS in a fixed order.  T = 4096, H = 4096: 41 us for 67 MB, the
+// matrix instructions 14 of them.  Bound by latency: the compiler makes the loads of
+// d_logits conditional and waits for each, nothing is asked for ahead (the bf16 kernel
+// below is rid of that by bounded loads).
 typedef float f32x4v __attribute__((ext_vector_type(4)));
 constexpr int kWgWaves = 16;
 constexpr int kWgCols = 64;

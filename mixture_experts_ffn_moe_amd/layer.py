@@ -13,7 +13,8 @@ def _dtype(shape) -> torch.dtype:
 
 
 def workspace_views(shape, ws: torch.Tensor) -> dict:
-    """Views of the intermediates moe_forward leaves in workspace `ws` (uint8)."""
+    """Views of the intermediates moe_forward (or moe_forward_q4) leaves in workspace `ws` (uint8).  The small-token
+    path writes no y: its view then holds what was there before."""
     L = moe_get_workspace_layout(shape)
     T, E, k, H = shape.T, shape.E, shape.k, shape.H
     R = T * k

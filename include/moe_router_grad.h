@@ -23,7 +23,8 @@
  * (NaN, infinities, ids out of range).  NULL: every token is valid.
  * For the other tokens, logits, weights and gradients are finite, except
  * that a logit may be -infinity (an expert switched off: probability 0); a
- * row without any finite logit has probability 0 everywhere.  topk_ids and
+ * row without any finite logit has probability 0 everywhere (moe_route gives no
+ * finite weights for such a row: mask it, or pass weights of 0).  topk_ids and
  * topk_w are moe_route's: the k ids of a token are distinct and in [0, E) (an id
  * outside that range is skipped: nothing is read or written out of bounds,
  * and the result is then unspecified).

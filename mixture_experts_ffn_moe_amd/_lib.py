@@ -34,6 +34,11 @@ EXPORTED = (
     # router gradients (moe_router_grad.h)
     "moe_balance_workspace_size", "moe_balance_loss", "moe_route_backward",
     "moe_router_grad_workspace_size", "moe_router_weight_grad", "moe_finalize_backward",
+    # shared expert's training and dropout (moe_shared_train.h)
+    "moe_dropout_add", "moe_dropout_backward", "moe_shared_ffn_train", "moe_shared_backward_workspace_size",
+    "moe_shared_ffn_backward",
+    # request adapters (moe_lora.h)
+    "moe_lora_workspace_size", "moe_lora_w13_swiglu", "moe_lora_down", "moe_shared_ffn_lora",
     # measurement probes (moe_probe.h)
     "moe_probe_mfma_bf16", "moe_probe_mfma_flops", "moe_probe_read",
 )
@@ -67,6 +72,10 @@ class MoeQ4Spec(ctypes.Structure):
 
 class MoeQ4Sizes(ctypes.Structure):
     _fields_ = [(n, ctypes.c_size_t) for n in ("w1_codes", "w1_scales", "w2_codes", "w2_scales")]
+
+
+class MoeLoraSpec(ctypes.Structure):
+    _fields_ = [("adapters", ctypes.c_int32), ("rank", ctypes.c_int32)]
 
 
 def _load():
@@ -128,6 +137,22 @@ def _load():
     lib.moe_router_weight_grad.restype = i32
     lib.moe_finalize_backward.argtypes = [S, P, P, P, P, P]
     lib.moe_finalize_backward.restype = i32
+    f64, size = ctypes.c_double, ctypes.c_size_t
+    A = ctypes.POINTER(MoeLoraSpec)
+    lib.moe_dropout_add.argtypes = [S, f64, P, P, P, P, P]
+    lib.moe_dropout_backward.argtypes = [S, f64, P, P, P, P]
+    lib.moe_shared_ffn_train.argtypes = [S, i32, f64] + [P] * 9
+    lib.moe_shared_backward_workspace_size.argtypes = [S, i32]
+    lib.moe_shared_ffn_backward.argtypes = [S, i32, f64] + [P] * 11 + [size, P]
+    lib.moe_lora_workspace_size.argtypes = [S, i32, A]
+    lib.moe_lora_w13_swiglu.argtypes = [S, i32, A] + [P] * 8 + [size, P]
+    lib.moe_lora_down.argtypes = [S, i32, A] + [P] * 9 + [size, P]
+    lib.moe_shared_ffn_lora.argtypes = [S, i32, A] + [P] * 13 + [size, P]
+    for f in (lib.moe_dropout_add, lib.moe_dropout_backward, lib.moe_shared_ffn_train, lib.moe_shared_ffn_backward,
+              lib.moe_lora_w13_swiglu, lib.moe_lora_down, lib.moe_shared_ffn_lora):
+        f.restype = i32
+    lib.moe_shared_backward_workspace_size.restype = size
+    lib.moe_lora_workspace_size.restype = size
     lib.moe_probe_mfma_bf16.argtypes = [i32, P, P]
     lib.moe_probe_mfma_bf16.restype = i32
     lib.moe_probe_mfma_flops.argtypes = [i32]
@@ -508,6 +533,120 @@ def moe_finalize_backward(shape, y, inv, d_out, d_topk_w, stream=None):
             _arg("d_out", d_out, _layer_dtype(shape), T * H), _arg("d_topk_w", d_topk_w, torch.float32, R))
     _on_current(y, inv, d_out, d_topk_w, stream=stream)
     _check(lib.moe_finalize_backward(ctypes.byref(shape), *args, _stream(stream)), "moe_finalize_backward")
+
+
+# ---- shared expert's training and dropout (moe_shared_train.h)
+
+
+def _rng_arg(p, rng):
+    """The random stream's seed and offset (an int64 tensor of two on the GPU); unread where nothing is dropped."""
+    return _arg("rng", rng, torch.int64, 2, nullable=not p >= 1 / 131072)
+
+
+def moe_dropout_add(shape, p, rng, y, residual, out, stream=None):
+    """out = residual (or None) + dropout(y); rng: int64 [2] on the GPU, seed and offset."""
+    n, dt = shape.T * shape.H, _layer_dtype(shape)
+    args = (_rng_arg(p, rng), _arg("y", y, dt, n), _arg("residual", residual, dt, n, nullable=True),
+            _arg("out", out, dt, n))
+    _on_current(rng, y, residual, out, stream=stream)
+    _check(lib.moe_dropout_add(ctypes.byref(shape), float(p), *args, _stream(stream)), "moe_dropout_add")
+
+
+def moe_dropout_backward(shape, p, rng, d_out, d_y, stream=None):
+    """Gradient of moe_dropout_add's y, with the forward call's p and rng."""
+    n, dt = shape.T * shape.H, _layer_dtype(shape)
+    args = (_rng_arg(p, rng), _arg("d_out", d_out, dt, n), _arg("d_y", d_y, dt, n))
+    _on_current(rng, d_out, d_y, stream=stream)
+    _check(lib.moe_dropout_backward(ctypes.byref(shape), float(p), *args, _stream(stream)), "moe_dropout_backward")
+
+
+def moe_shared_ffn_train(shape, Is, p, rng, x, w1s, w2s, residual, gu, hs, out, stream=None):
+    """The shared expert's forward pass with dropout of its hidden values; keeps gu and hs for the backward pass."""
+    T, H, dt = shape.T, shape.H, _layer_dtype(shape)
+    args = (_rng_arg(p, rng), _arg("x", x, dt, T * H), _arg("w1s", w1s, dt, 2 * Is * H), _arg("w2s", w2s, dt, H * Is),
+            _arg("residual", residual, dt, T * H, nullable=True), _arg("gu", gu, dt, T * 2 * Is),
+            _arg("hs", hs, dt, T * Is), _arg("out", out, dt, T * H))
+    _on_current(rng, x, w1s, w2s, residual, gu, hs, out, stream=stream)
+    _check(lib.moe_shared_ffn_train(ctypes.byref(shape), int(Is), float(p), *args, _stream(stream)),
+           "moe_shared_ffn_train")
+
+
+def moe_shared_backward_workspace_size(shape: MoeShape, Is: int) -> int:
+    return int(lib.moe_shared_backward_workspace_size(ctypes.byref(shape), int(Is)))
+
+
+def moe_shared_ffn_backward(shape, Is, p, rng, x, w1s, w2s, gu, hs, d_out, d_x, d_w1s, d_w2s, workspace, stream=None):
+    """Gradients of x (unless d_x is None) and of both weights (unless d_w1s and d_w2s are None)."""
+    T, H, dt = shape.T, shape.H, _layer_dtype(shape)
+    no_x, no_w = d_x is None, d_w1s is None and d_w2s is None
+    args = (_rng_arg(p, rng), _arg("x", x, dt, T * H, nullable=no_w), _arg("w1s", w1s, dt, 2 * Is * H, nullable=no_x),
+            _arg("w2s", w2s, dt, H * Is), _arg("gu", gu, dt, T * 2 * Is), _arg("hs", hs, dt, T * Is, nullable=no_w),
+            _arg("d_out", d_out, dt, T * H), _arg("d_x", d_x, dt, T * H, nullable=True),
+            _arg("d_w1s", d_w1s, dt, 2 * Is * H, nullable=True), _arg("d_w2s", d_w2s, dt, H * Is, nullable=True))
+    ws, nbytes = _workspace(workspace)
+    _on_current(rng, x, w1s, w2s, gu, hs, d_out, d_x, d_w1s, d_w2s, workspace, stream=stream)
+    _check(lib.moe_shared_ffn_backward(ctypes.byref(shape), int(Is), float(p), *args, ws, nbytes, _stream(stream)),
+           "moe_shared_ffn_backward")
+
+
+# ---- request adapters (moe_lora.h)
+
+
+def make_lora(adapters, rank) -> MoeLoraSpec:
+    """A set of `adapters` low-rank adapters of one rank (a multiple of 8)."""
+    return MoeLoraSpec(adapters, rank)
+
+
+def moe_lora_workspace_size(shape: MoeShape, Is: int, lora: MoeLoraSpec) -> int:
+    return int(lib.moe_lora_workspace_size(ctypes.byref(shape), int(Is), ctypes.byref(lora)))
+
+
+def _w13_adapters(lora, Is, H, dt, a1, b1):
+    n = lora.adapters * lora.rank
+    return _arg("a1", a1, dt, n * H), _arg("b1", b1, dt, n * 2 * Is)
+
+
+def _down_adapters(lora, Is, H, dt, a2, b2):
+    n = lora.adapters * lora.rank
+    return _arg("a2", a2, dt, n * Is), _arg("b2", b2, dt, n * H)
+
+
+def moe_lora_w13_swiglu(shape, Is, lora, x, w1s, a1, b1, scale, adapter_ids, hs, workspace, stream=None):
+    """SwiGLU of the shared expert's gate and up projection, every token with its own adapter."""
+    T, H, dt = shape.T, shape.H, _layer_dtype(shape)
+    args = (_arg("x", x, dt, T * H), _arg("w1s", w1s, dt, 2 * Is * H), *_w13_adapters(lora, Is, H, dt, a1, b1),
+            _arg("scale", scale, torch.float32, lora.adapters), _arg("adapter_ids", adapter_ids, torch.int32, T),
+            _arg("hs", hs, dt, T * Is))
+    ws, nbytes = _workspace(workspace)
+    _on_current(x, w1s, a1, b1, scale, adapter_ids, hs, workspace, stream=stream)
+    _check(lib.moe_lora_w13_swiglu(ctypes.byref(shape), int(Is), ctypes.byref(lora), *args, ws, nbytes,
+                                   _stream(stream)), "moe_lora_w13_swiglu")
+
+
+def moe_lora_down(shape, Is, lora, hs, w2s, a2, b2, scale, adapter_ids, residual, out, workspace, stream=None):
+    """The shared expert's down projection, every token with its own adapter, plus the residual (or None)."""
+    T, H, dt = shape.T, shape.H, _layer_dtype(shape)
+    args = (_arg("hs", hs, dt, T * Is), _arg("w2s", w2s, dt, H * Is), *_down_adapters(lora, Is, H, dt, a2, b2),
+            _arg("scale", scale, torch.float32, lora.adapters), _arg("adapter_ids", adapter_ids, torch.int32, T),
+            _arg("residual", residual, dt, T * H, nullable=True), _arg("out", out, dt, T * H))
+    ws, nbytes = _workspace(workspace)
+    _on_current(hs, w2s, a2, b2, scale, adapter_ids, residual, out, workspace, stream=stream)
+    _check(lib.moe_lora_down(ctypes.byref(shape), int(Is), ctypes.byref(lora), *args, ws, nbytes, _stream(stream)),
+           "moe_lora_down")
+
+
+def moe_shared_ffn_lora(shape, Is, lora, x, w1s, w2s, a1, b1, a2, b2, scale, adapter_ids, residual, hs, out, workspace,
+                        stream=None):
+    """The shared expert with adapters on both projections, plus the residual (or None)."""
+    T, H, dt = shape.T, shape.H, _layer_dtype(shape)
+    args = (_arg("x", x, dt, T * H), _arg("w1s", w1s, dt, 2 * Is * H), _arg("w2s", w2s, dt, H * Is),
+            *_w13_adapters(lora, Is, H, dt, a1, b1), *_down_adapters(lora, Is, H, dt, a2, b2),
+            _arg("scale", scale, torch.float32, lora.adapters), _arg("adapter_ids", adapter_ids, torch.int32, T),
+            _arg("residual", residual, dt, T * H, nullable=True), _arg("hs", hs, dt, T * Is), _arg("out", out, dt, T * H))
+    ws, nbytes = _workspace(workspace)
+    _on_current(x, w1s, w2s, a1, b1, a2, b2, scale, adapter_ids, residual, hs, out, workspace, stream=stream)
+    _check(lib.moe_shared_ffn_lora(ctypes.byref(shape), int(Is), ctypes.byref(lora), *args, ws, nbytes,
+                                   _stream(stream)), "moe_shared_ffn_lora")
 
 
 def moe_probe_mfma_bf16(iterations: int, sink, stream=None) -> float:

@@ -1,0 +1,449 @@
+// Tiled matrix products of the shared expert's training step and of its
+// request adapters (gfx950).
+//
+//   C[m, n] = sum_k A(m, k) B(n, k),  bf16 or fp32 elements, fp32 sums.
+//
+// Either operand is stored with k contiguous (rows of k: x, weights in the
+// forward pass) or with k as the row index ("k-rows": weights where the
+// gradient runs back through them, both operands of a weight gradient).
+//   * global -> LDS copies are direct (dma16), a ring of SLOTS k-tiles of 128
+//     bytes of k a row.  A k-contiguous tile holds 128-byte rows whose 16-byte
+//     chunks are XOR-swizzled by row; a k-rows tile holds BK rows of the
+//     tile's columns, swizzled in units of 16 columns.
+//   * operands of k-rows tiles are transposed on the way out of LDS: bf16 by
+//     the transposing 8-byte read (16 lanes give the addresses of four rows
+//     of 16 columns, lane i receives column i of the four rows), fp32 by
+//     4-byte reads.  No transposed copy of anything is ever written.
+//   * the second matrix operand is A, so a lane holds consecutive columns n
+//     of one row m; the finished tile passes through LDS in strips of F rows
+//     per wave (the wave's own region: no workgroup barrier) and each lane
+//     finishes 8 consecutive columns with 16-byte loads and stores.
+// Every row, column and k index that would lie outside an operand is clamped
+// to its last one; what was read for them is masked (k) or never stored.
+#pragma once
+
+#include "moe_common.h"
+
+namespace moe {
+namespace tile {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// Matrix instruction for F x F blocks: SUB k-values of one call, 16 bytes of
+// each operand a lane (row lane % F, 16-byte chunk lane / F of the SUB values).
+template <class E, int F>
+struct Mma;
+template <>
+struct Mma<uint16_t, 32> {
+  typedef bf16x8 frag;
+  typedef f32x16 acc;
+  static constexpr int SUB = 16;
+  static __device__ __forceinline__ acc mul(frag a, frag b, acc c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<uint16_t, 16> {
+  typedef bf16x8 frag;
+  typedef f32x4 acc;
+  static constexpr int SUB = 32;
+  static __device__ __forceinline__ acc mul(frag a, frag b, acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <>
+struct Mma<float, 16> {
+  typedef f32x4 frag;
+  typedef f32x4 acc;
+  static constexpr int SUB = 16;
+  // call s contracts the k-values 4 * (lane / 16) + s of both operands
+  static __device__ __forceinline__ acc mul(frag a, frag b, acc c) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], c, 0, 0, 0);
+    return c;
+  }
+};
+
+// Operand of a product: rows (of k) or, k-rows, columns of a [K, count] matrix.
+struct Operand {
+  const void* p;
+  int ld;     // elements between rows
+  int count;  // rows m (or n), k-rows: columns
+};
+
+template <class E_, int BM_, int BN_, int WM_, int WN_, int F_, int SLOTS_, bool TA_, bool TB_>
+struct Cfg {
+  typedef E_ E;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, F = F_, SLOTS = SLOTS_;
+  static constexpr bool TA = TA_, TB = TB_;  // operand stored as k-rows
+  typedef Mma<E, F> M;
+  static constexpr int ES = sizeof(E), BK = 128 / ES, EPC = 16 / ES;  // elements of a 16-byte chunk
+  static constexpr int NW = WM * WN, NTHR = NW * 64;
+  static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / F, FN = TN / F;
+  static constexpr int NSUB = BK / M::SUB, CPS = 64 / F;  // substeps of a k-tile, chunks of a substep
+  static constexpr int AQ = BM / 8 / NW, BQ = BN / 8 / NW;  // 1 KB copies a wave makes of a k-tile
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, SLOT_BYTES = A_BYTES + B_BYTES;
+  static constexpr int STRIP_LD = TN + 4;  // floats
+  static constexpr int STRIP_BYTES = F * STRIP_LD * 4;
+  static constexpr int LDS_BYTES = SLOTS * SLOT_BYTES > NW * STRIP_BYTES ? SLOTS * SLOT_BYTES : NW * STRIP_BYTES;
+  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && TM % F == 0 && TN % F == 0, "tile split");
+  static_assert(SLOTS >= 2 && (SLOTS - 2) * (AQ + BQ) < 64, "vmcnt");
+  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+};
+
+// Swizzle of a k-contiguous tile: 16 rows read together hit 16 distinct
+// 16-byte slots of the 256 bytes that LDS serves at once.
+__device__ __forceinline__ int swz_row(int row) { return (row >> 1) & 7; }
+
+// Swizzle of a k-rows tile of C columns: XOR of the 16-column unit of row k.
+// 32 lanes of a bf16 read take four rows (F = 32: of two adjacent units) or
+// eight (F = 16: k and k + 8, of one unit); the XOR sends them to the eight
+// 32-byte slots of 256 bytes.  fp32 reads take four rows, four apart.
+template <class E, int F, int C>
+__device__ __forceinline__ int swz_k(int k) {
+  if (sizeof(E) == 4) return (k >> 2) & 3;
+  if (F == 32) return C >= 128 ? (k & 3) << 1 : k & 2;
+  return C >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
+}
+
+// Source byte offsets of a wave's direct copies of one operand tile, relative
+// to the tile's base (the first row's, k-rows: first column's, at the current
+// k-tile).  C rows or columns from `first`, at most `count` of them exist.
+// `map` (may be null): stored row of a logical row.
+// k_left: k-values from the k-tile's start to the end of K.
+template <class C, bool KROWS, int N, int Q, class Row>
+__device__ __forceinline__ void copy_offsets(uint32_t (&off)[Q], int first, int count, int ld, int k_left,
+                                             int wave, int lane, Row row_of) {
+  typedef typename C::E E;
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const int q = wave + C::NW * i;
+    if (!KROWS) {
+      const int row = q * 8 + (lane >> 3);
+      int c = (lane & 7) ^ swz_row(row);
+      if (c * C::EPC >= k_left) c = 0;
+      off[i] = ((uint32_t)row_of(row) * (uint32_t)ld + (uint32_t)(c * C::EPC)) * C::ES;
+    } else {
+      constexpr int CPR = N * C::ES / 16;  // chunks of a k-row
+      constexpr int UC = C::ES;            // chunks of a 16-column unit
+      const int k = q * (64 / CPR) + lane / CPR;
+      const int c = lane % CPR;
+      int n = (((c / UC) ^ swz_k<E, C::F, N>(k)) * UC + c % UC) * C::EPC;
+      n = min(n, count - first - C::EPC);
+      off[i] = ((uint32_t)min(k, k_left - 1) * (uint32_t)ld + (uint32_t)n) * C::ES;
+    }
+  }
+}
+
+// Operand fragment of substep ks from an LDS tile: rows r0 .. r0 + F.
+template <class C, bool KROWS, int N>
+__device__ __forceinline__ typename C::M::frag read_frag(const char* t, int r0, int ks, int lane) {
+  typedef typename C::E E;
+  if constexpr (!KROWS) {
+    const int row = r0 + lane % C::F;
+    const int c = (ks * C::CPS + lane / C::F) ^ swz_row(row);
+    return *reinterpret_cast<const typename C::M::frag*>(t + row * 128 + c * 16);
+  } else if constexpr (C::ES == 2) {
+    const int g = lane >> 4, i = lane & 15;
+    const int unit = r0 / 16 + (C::F == 32 ? (g & 1) : 0);
+    const int k0 = ks * C::M::SUB + 8 * (C::F == 32 ? g >> 1 : g) + (i >> 2);
+    typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+    union {
+      s16x4 h[2];
+      bf16x8 v;
+    } u;
+    const char* a = t + k0 * (N * 2) + ((unit ^ swz_k<E, C::F, N>(k0)) * 32) + (i & 3) * 8;
+    // k0 + 4 has the same swizzle
+    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a));
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + 4 * (N * 2)));
+    return u.v;
+  } else {
+    const int k0 = ks * C::M::SUB + 4 * (lane >> 4);
+    f32x4 v;
+    const char* a = t + k0 * (N * 4) + ((r0 / 16) ^ swz_k<E, C::F, N>(k0)) * 64 + (lane & 15) * 4;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) v[s] = *reinterpret_cast<const float*>(a + s * (N * 4));
+    return v;
+  }
+}
+
+// Zeroes the k-values at and past `left` (k-values from the substep's start).
+template <class C>
+__device__ __forceinline__ typename C::M::frag mask_k(typename C::M::frag f, int left, int lane) {
+  constexpr int N = 16 / C::ES;
+  const int mine = left - N * (lane / C::F);
+#pragma unroll
+  for (int e = 0; e < N; ++e)
+    if (e >= mine) f[e] = 0.0f;
+  return f;
+}
+
+__device__ __forceinline__ void slot_barrier() {
+  __builtin_amdgcn_s_waitcnt(0xF | (7 << 4) | (0 << 8) | (3 << 14));  // lgkmcnt(0)
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_barrier" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Wait states between a matrix instruction and the first vector instruction
+// that reads its result, where a branch lies between them: the compiler counts
+// them within a block only.
+__device__ __forceinline__ void settle() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Tile of this workgroup.  Block b runs on die b % 8; each die takes a
+// contiguous range of tiles, which run down groups of 8 row tiles, so that
+// the 32 tiles a die works on at a time share their rows and columns in its L2.
+__device__ __forceinline__ bool tile_of(int b, int mt, int nt, int& m, int& n) {
+  const int all = mt * nt, per = (all + kXcds - 1) / kXcds;
+  const int slot = b / kXcds, t = (b % kXcds) * per + slot;
+  if (slot >= per || t >= all) return false;
+  constexpr int G = 8;
+  const int group = t / (G * nt), in = t - group * (G * nt);
+  const int rows = min(G, mt - group * G);
+  m = group * G + in % rows;
+  n = in / rows;
+  return true;
+}
+
+struct Identity {
+  __device__ __forceinline__ int operator()(int r) const { return r; }
+};
+
+// No low-rank addition.
+struct NoExtra {
+  static constexpr bool ON = false;
+  __device__ __forceinline__ int a_row(int r) const { return r; }
+  __device__ __forceinline__ int out_row(int r) const { return r; }
+};
+
+// One product.  PAIR: B has two halves of `half` rows (gate, up) and a tile
+// takes BN / 2 columns of each; the epilogue then gets both values of a column.
+template <class C, class Epi, class Extra>
+__device__ __forceinline__ void product(const Operand A, const Operand B, int K, int half, int tm, int tn,
+                                        const Epi& epi, const Extra& extra, char* smem) {
+  constexpr bool PAIR = Epi::PAIR;
+  constexpr int OC = PAIR ? C::BN / 2 : C::BN;  // output columns of a tile
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / C::WN, wn = wave % C::WN;
+  const int m0 = tm * C::BM, n0 = tn * OC;
+  const int N = PAIR ? half : B.count;
+  const int KT = (K + C::BK - 1) / C::BK;
+
+  // bases of the tile (k-tile 0) and the row maps below them
+  const bool rowmap = Extra::ON;
+  const char* a0 = (const char*)A.p + (C::TA ? (size_t)m0 : rowmap ? 0 : (size_t)m0 * A.ld) * C::ES;
+  const char* b0 = (const char*)B.p + (C::TB ? (size_t)n0 : PAIR ? 0 : (size_t)n0 * B.ld) * C::ES;
+  auto arow = [&](int r) {
+    const int g = min(m0 + r, A.count - 1);
+    return rowmap ? extra.a_row(g) : g - m0;
+  };
+  auto brow = [&](int r) {
+    if (!PAIR) return min(n0 + r, B.count - 1) - n0;
+    const int up = r >= C::BN / 2;
+    return up * half + min(n0 + r - up * (C::BN / 2), half - 1);
+  };
+  const size_t a_step = C::TA ? (size_t)C::BK * A.ld * C::ES : (size_t)128;
+  const size_t b_step = C::TB ? (size_t)C::BK * B.ld * C::ES : (size_t)128;
+  uint32_t aoff[C::AQ], boff[C::BQ];
+  copy_offsets<C, C::TA, C::BM>(aoff, m0, A.count, A.ld, K, wave, lane, arow);
+  copy_offsets<C, C::TB, C::BN>(boff, n0, B.count, B.ld, K, wave, lane, brow);
+
+  const uint32_t lds = (uint32_t)(uintptr_t)smem;
+  auto issue = [&](int kt) {
+    if (kt == KT - 1 && kt > 0 && K % C::BK != 0) {  // the last k-tile is short
+      copy_offsets<C, C::TA, C::BM>(aoff, m0, A.count, A.ld, K - kt * C::BK, wave, lane, arow);
+      copy_offsets<C, C::TB, C::BN>(boff, n0, B.count, B.ld, K - kt * C::BK, wave, lane, brow);
+    }
+    const uint32_t s = lds + (uint32_t)((kt % C::SLOTS) * C::SLOT_BYTES);
+    const char* pa = uniform_ptr(a0 + kt * a_step);
+    const char* pb = uniform_ptr(b0 + kt * b_step);
+#pragma unroll
+    for (int i = 0; i < C::AQ; ++i) dma16(s + (uint32_t)(wave + C::NW * i) * 1024u, pa, aoff[i]);
+#pragma unroll
+    for (int i = 0; i < C::BQ; ++i) dma16(s + C::A_BYTES + (uint32_t)(wave + C::NW * i) * 1024u, pb, boff[i]);
+  };
+
+  typename C::M::acc acc[C::FM][C::FN];
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int e = 0; e < C::F * C::F / 64; ++e) acc[i][j][e] = 0.0f;
+
+  auto b_r0 = [&](int j) {
+    if (!PAIR) return wn * C::TN + C::F * j;
+    return j < C::FN / 2 ? wn * (C::TN / 2) + C::F * j : C::BN / 2 + wn * (C::TN / 2) + C::F * (j - C::FN / 2);
+  };
+  static_assert(!PAIR || C::FN % 2 == 0, "gate and up fragments of a wave");
+
+#pragma unroll
+  for (int s = 0; s < C::SLOTS - 1; ++s)
+    if (s < KT) issue(s);
+  constexpr int LEAD = (C::SLOTS - 2) * (C::AQ + C::BQ);
+  // k-tile kt has landed, and the slot of k-tile kt - 1 is free again
+  auto advance = [&](int kt) {
+    if (kt + C::SLOTS - 2 < KT)
+      wait_vmcnt<LEAD>();
+    else
+      wait_vmcnt<0>();
+    slot_barrier();
+    if (kt + C::SLOTS - 1 < KT) issue(kt + C::SLOTS - 1);
+  };
+  auto substep = [&](const char* ta, int ks, auto mask) {
+    const char* tb = ta + C::A_BYTES;
+    typename C::M::frag fa[C::FM], fb[C::FN];
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) fa[i] = mask(read_frag<C, C::TA, C::BM>(ta, wm * C::TM + C::F * i, ks, lane));
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) fb[j] = mask(read_frag<C, C::TB, C::BN>(tb, b_r0(j), ks, lane));
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) acc[i][j] = C::M::mul(fb[j], fa[i], acc[i][j]);
+  };
+  typedef typename C::M::frag Frag;
+  const int KF = K / C::BK;
+  for (int kt = 0; kt < KF; ++kt) {
+    advance(kt);
+#pragma unroll
+    for (int ks = 0; ks < C::NSUB; ++ks) substep(smem + (kt % C::SLOTS) * C::SLOT_BYTES, ks, [](Frag f) { return f; });
+  }
+  if (KF < KT) {
+    advance(KF);
+    const int left = K - KF * C::BK;
+    for (int ks = 0; ks * C::M::SUB < left; ++ks)
+      substep(smem + (KF % C::SLOTS) * C::SLOT_BYTES, ks,
+              [&](Frag f) { return mask_k<C>(f, left - ks * C::M::SUB, lane); });
+  }
+  if constexpr (Extra::ON) extra.template add<C>(acc, m0 + wm * C::TM, [&](int j) {
+    const int r = b_r0(j) + lane % C::F;
+    if (!PAIR) return min(n0 + r, N - 1);
+    const int up = r >= C::BN / 2;
+    return up * half + min(n0 + r - up * (C::BN / 2), half - 1);
+  }, lane);
+
+  settle();
+  __syncthreads();  // every wave is past its last LDS read: the ring is free
+  float* strip = reinterpret_cast<float*>(smem + wave * C::STRIP_BYTES);
+  constexpr int WC = PAIR ? C::TN / 2 : C::TN;  // output columns of the wave
+  constexpr int LPR = WC / 8, RPI = 64 / LPR;   // lanes of a row, rows of an iteration
+  constexpr int ITER = (C::F + RPI - 1) / RPI;   // RPI > F: the last lanes have no row
+  static_assert(WC % 8 == 0 && 64 % LPR == 0 && (C::F % RPI == 0 || RPI % C::F == 0), "epilogue split");
+  const int c8 = (lane % LPR) * 8, col = n0 + wn * WC + c8;
+#pragma unroll
+  for (int i = 0; i < C::FM; ++i) {
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+      for (int q = 0; q < C::F * C::F / 256; ++q) {
+        const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        *reinterpret_cast<f32x4*>(strip + (lane % C::F) * C::STRIP_LD + C::F * j + 8 * q + 4 * (lane / C::F)) = v;
+      }
+    __builtin_amdgcn_wave_barrier();
+    typename Epi::Pre pre[ITER];
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+      const int r = it * RPI + lane / LPR, row = m0 + wm * C::TM + C::F * i + r;
+      if (r < C::F && row < A.count && col < N) pre[it] = epi.load(extra.out_row(row), col);
+    }
+#pragma unroll
+    for (int it = 0; it < ITER; ++it) {
+      const int r = it * RPI + lane / LPR, row = m0 + wm * C::TM + C::F * i + r;
+      const float* s = strip + (RPI > C::F ? r % C::F : r) * C::STRIP_LD + c8;
+      f32x4 v[4];
+      v[0] = *reinterpret_cast<const f32x4*>(s);
+      v[1] = *reinterpret_cast<const f32x4*>(s + 4);
+      if (PAIR) {
+        v[2] = *reinterpret_cast<const f32x4*>(s + WC);
+        v[3] = *reinterpret_cast<const f32x4*>(s + WC + 4);
+      }
+      if (r < C::F && row < A.count && col < N) epi.store(extra.out_row(row), col, v, pre[it]);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <class C, class Epi, class Extra>
+__global__ __launch_bounds__(C::NTHR, 1) void product_kernel(Operand A, Operand B, int K, int half, int mt, int nt,
+                                                             Epi epi, Extra extra) {
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS_BYTES];
+  int tm, tn;
+  if (!tile_of(blockIdx.x, mt, nt, tm, tn)) return;
+  product<C, Epi, Extra>(A, B, K, half, tm, tn, epi, extra, smem);
+}
+
+template <class C, class Epi, class Extra = NoExtra>
+hipError_t launch_product(Operand A, Operand B, int K, int half, const Epi& epi, hipStream_t st,
+                          const Extra& extra = Extra{}) {
+  const int oc = Epi::PAIR ? C::BN / 2 : C::BN, N = Epi::PAIR ? half : B.count;
+  const int mt = (A.count + C::BM - 1) / C::BM, nt = (N + oc - 1) / oc;
+  const unsigned grid = (unsigned)(((long long)mt * nt + kXcds - 1) / kXcds * kXcds);
+  hipLaunchKernelGGL((product_kernel<C, Epi, Extra>), dim3(grid), dim3(C::NTHR), 0, st, A, B, K, half, mt, nt, epi,
+                     extra);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Eight consecutive elements of a row: one 16-byte vector of bf16, two of fp32.
+template <class E>
+struct Vec8;
+template <>
+struct Vec8<uint16_t> {
+  uint4 d;
+  __device__ __forceinline__ void load(const uint16_t* p) { d = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ float operator[](int i) const {
+    const uint32_t w = i < 2 ? d.x : i < 4 ? d.y : i < 6 ? d.z : d.w;
+    return (i & 1) ? __uint_as_float(w & 0xffff0000u) : __uint_as_float(w << 16);
+  }
+};
+template <>
+struct Vec8<float> {
+  f32x4 d[2];
+  __device__ __forceinline__ void load(const float* p) {
+    d[0] = reinterpret_cast<const f32x4*>(p)[0];
+    d[1] = reinterpret_cast<const f32x4*>(p)[1];
+  }
+  __device__ __forceinline__ float operator[](int i) const { return d[i >> 2][i & 3]; }
+};
+__device__ __forceinline__ void store8(uint16_t* p, f32x4 a, f32x4 b) {
+  const uint2 lo = pack_bf16x4(a), hi = pack_bf16x4(b);
+  *reinterpret_cast<uint4*>(p) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+}
+__device__ __forceinline__ void store8(float* p, f32x4 a, f32x4 b) {
+  reinterpret_cast<f32x4*>(p)[0] = a;
+  reinterpret_cast<f32x4*>(p)[1] = b;
+}
+
+// out[row, col] = v (+ residual)
+template <class E>
+struct StoreOut {
+  static constexpr bool PAIR = false;
+  E* out;
+  const E* residual;  // may be null
+  int ld;
+  struct Pre {
+    Vec8<E> r;
+  };
+  __device__ __forceinline__ Pre load(int row, int col) const {
+    Pre p;
+    if (residual) p.r.load(residual + (size_t)row * ld + col);
+    return p;
+  }
+  __device__ __forceinline__ void store(int row, int col, f32x4* v, const Pre& p) const {
+    if (residual) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i >> 2][i & 3] += p.r[i];
+    }
+    store8(out + (size_t)row * ld + col, v[0], v[1]);
+  }
+};
+
+}  // namespace tile
+}  // namespace moe

@@ -56,12 +56,12 @@ moe_status moe_dropout_backward(const moe_shape* shape, double p, const uint64_t
  *   hs[t, i]  = dropout(SiLU(gate[t, i]) * up[t, i])             (its index t*Is + i)
  *   out[t, n] = sum_i hs[t, i] * w2s[n, i] + residual[t, n]
  * x, out [T, H], w1s [2*Is, H], w2s [H, Is] as in moe_shared.h; gu [T, 2*Is]
- * and hs [T, Is] are kept for the backward pass; all in dtype, each rounded
- * once (hs from the unrounded gate and up).  residual [T, H] may be NULL; out
+ * (fp32) and hs [T, Is] are kept for the backward pass; hs and out in dtype,
+ * each rounded once.  residual [T, H] may be NULL; out
  * may be residual.  T == 0 enqueues nothing. */
 moe_status moe_shared_ffn_train(const moe_shape* shape, int32_t Is, double p, const uint64_t* rng,
                                 const void* x, const void* w1s, const void* w2s,
-                                const void* residual, void* gu, void* hs, void* out, void* stream);
+                                const void* residual, float* gu, void* hs, void* out, void* stream);
 
 /* Workspace bytes of moe_shared_ffn_backward, or 0 if shape or Is is invalid
  * or unsupported.  Pure host function. */
@@ -82,7 +82,7 @@ size_t moe_shared_backward_workspace_size(const moe_shape* shape, int32_t Is);
  *   workspace: moe_shared_backward_workspace_size bytes, 256-byte aligned. */
 moe_status moe_shared_ffn_backward(const moe_shape* shape, int32_t Is, double p,
                                    const uint64_t* rng, const void* x, const void* w1s,
-                                   const void* w2s, const void* gu, const void* hs,
+                                   const void* w2s, const float* gu, const void* hs,
                                    const void* d_out, void* d_x, void* d_w1s, void* d_w2s,
                                    void* workspace, size_t workspace_bytes, void* stream);
 

@@ -561,10 +561,10 @@ def moe_dropout_backward(shape, p, rng, d_out, d_y, stream=None):
 
 
 def moe_shared_ffn_train(shape, Is, p, rng, x, w1s, w2s, residual, gu, hs, out, stream=None):
-    """The shared expert's forward pass with dropout of its hidden values; keeps gu and hs for the backward pass."""
+    """The shared expert's forward pass with dropout of its hidden values; keeps gu (fp32) and hs for the backward pass."""
     T, H, dt = shape.T, shape.H, _layer_dtype(shape)
     args = (_rng_arg(p, rng), _arg("x", x, dt, T * H), _arg("w1s", w1s, dt, 2 * Is * H), _arg("w2s", w2s, dt, H * Is),
-            _arg("residual", residual, dt, T * H, nullable=True), _arg("gu", gu, dt, T * 2 * Is),
+            _arg("residual", residual, dt, T * H, nullable=True), _arg("gu", gu, torch.float32, T * 2 * Is),
             _arg("hs", hs, dt, T * Is), _arg("out", out, dt, T * H))
     _on_current(rng, x, w1s, w2s, residual, gu, hs, out, stream=stream)
     _check(lib.moe_shared_ffn_train(ctypes.byref(shape), int(Is), float(p), *args, _stream(stream)),
@@ -580,7 +580,7 @@ def moe_shared_ffn_backward(shape, Is, p, rng, x, w1s, w2s, gu, hs, d_out, d_x, 
     T, H, dt = shape.T, shape.H, _layer_dtype(shape)
     no_x, no_w = d_x is None, d_w1s is None and d_w2s is None
     args = (_rng_arg(p, rng), _arg("x", x, dt, T * H, nullable=no_w), _arg("w1s", w1s, dt, 2 * Is * H, nullable=no_x),
-            _arg("w2s", w2s, dt, H * Is), _arg("gu", gu, dt, T * 2 * Is), _arg("hs", hs, dt, T * Is, nullable=no_w),
+            _arg("w2s", w2s, dt, H * Is), _arg("gu", gu, torch.float32, T * 2 * Is), _arg("hs", hs, dt, T * Is, nullable=no_w),
             _arg("d_out", d_out, dt, T * H), _arg("d_x", d_x, dt, T * H, nullable=True),
             _arg("d_w1s", d_w1s, dt, 2 * Is * H, nullable=True), _arg("d_w2s", d_w2s, dt, H * Is, nullable=True))
     ws, nbytes = _workspace(workspace)

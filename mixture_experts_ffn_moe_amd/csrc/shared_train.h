@@ -13,7 +13,7 @@ struct Ffn {
   bool bf16;
 };
 
-// gu [T, 2I] = x w1^T (gate, then up), hs [T, I] = dropout(SiLU(gate) * up)
+// gu [T, 2I] (fp32) = x w1^T (gate, then up), hs [T, I] = dropout(SiLU(gate) * up)
 hipError_t launch_train_w13(const Ffn& f, const Dropout& d, const void* x, const void* w1, void* gu, void* hs,
                             hipStream_t st);
 // out [T, H] = hs w2^T (+ residual)

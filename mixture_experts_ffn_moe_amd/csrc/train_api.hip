@@ -86,7 +86,7 @@ moe_status moe_dropout_backward(const moe_shape* shape, double p, const uint64_t
 }
 
 moe_status moe_shared_ffn_train(const moe_shape* shape, int32_t Is, double p, const uint64_t* rng, const void* x,
-                                const void* w1s, const void* w2s, const void* residual, void* gu, void* hs, void* out,
+                                const void* w1s, const void* w2s, const void* residual, float* gu, void* hs, void* out,
                                 void* stream) {
   Ffn f;
   Dropout d;
@@ -107,7 +107,7 @@ size_t moe_shared_backward_workspace_size(const moe_shape* shape, int32_t Is) {
 }
 
 moe_status moe_shared_ffn_backward(const moe_shape* shape, int32_t Is, double p, const uint64_t* rng, const void* x,
-                                   const void* w1s, const void* w2s, const void* gu, const void* hs,
+                                   const void* w1s, const void* w2s, const float* gu, const void* hs,
                                    const void* d_out, void* d_x, void* d_w1s, void* d_w2s, void* workspace,
                                    size_t workspace_bytes, void* stream) {
   Ffn f;

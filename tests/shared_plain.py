@@ -70,9 +70,7 @@ def ffn(x, w1, w2, residual, d_out, factors, dtype):
     if residual is not None:
         out = out + residual
         eo = eo + F32 * out.abs()
-    r = dict(gu=(z, _stored(z, ez, dtype)), hs=(h, eh), out=(out, _stored(out, eo, dtype)))
-    # gate and up as stored
-    eg, eu = _stored(g, eg, dtype), _stored(u, eu, dtype)
+    r = dict(gu=(z, ez), hs=(h, eh), out=(out, _stored(out, eo, dtype)))
     dh, ed = _mm(d_out, w2)
     dh, ed = factors * dh, factors * (ed + F32 * dh.abs())
     slope = s * (1 + g * (1 - s))

@@ -56,7 +56,7 @@ class Step:
         self.all = {}
         for n, dims in dict(gu=(T, 2 * Is), hs=(T, Is), out=(T, H), d_x=(T, H), d_w1s=(2 * Is, H), d_w2s=(H, Is)).items():
             k = int(np.prod(dims))
-            buf = torch.full((k + 512,), float("nan"), dtype=dt, device="cuda")
+            buf = torch.full((k + 512,), float("nan"), dtype=torch.float32 if n == "gu" else dt, device="cuda")
             self.all[n] = buf
             self.o[n] = buf[256:256 + k].view(*dims)
 
@@ -79,7 +79,7 @@ class Step:
     def check(self):
         torch.cuda.synchronize()
         for n, (v, e) in self.reference().items():
-            sp.check(n, self.o[n], v, e, self.dt)
+            sp.check(n, self.o[n], v, e, self.o[n].dtype)
         for n, b in self.all.items():
             assert torch.isnan(b[:256]).all() and torch.isnan(b[-256:]).all(), n
 

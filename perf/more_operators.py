@@ -248,7 +248,7 @@ def _own_ffn(s):
         s["shape"] = _shape(moe, case)
         s["workspace"] = torch.empty(moe.moe_shared_backward_workspace_size(s["shape"], Is), dtype=torch.uint8, device=DEV)
     e = lambda *dims: torch.empty(*dims, dtype=dt, device=DEV)  # noqa: E731
-    gu, hs, out = e(T, 2 * Is), e(T, Is), e(T, H)
+    gu, hs, out = torch.empty(T, 2 * Is, device=DEV), e(T, Is), e(T, H)
     d_x, d_w1, d_w2 = e(T, H), e(2 * Is, H), e(H, Is)
     moe.moe_shared_ffn_train(s["shape"], Is, case["p"], s["rng"], s["x"], s["w1"], s["w2"], s["residual"], gu, hs, out)
     moe.moe_shared_ffn_backward(s["shape"], Is, case["p"], s["rng"], s["x"], s["w1"], s["w2"], gu, hs, s["d_out"], d_x, d_w1, d_w2,

@@ -381,12 +381,12 @@ hipError_t big(const Ffn& f, const Lora& l, const void* x, int K, const void* w,
   const int half = Epi::PAIR ? rows / 2 : 0;
   auto tiles = [&](int bm, int bn) { return (long long)((f.T + bm - 1) / bm) * ((rows + bn - 1) / bn); };
   if constexpr (sizeof(E) == 2) {
-    if (tiles(256, 256) >= 192) return tile::launch_product<Cfg<E, 256, 256, 2, 4, 32, 2, false, false>>(A, B, K, half, epi, st, add);
-    if (tiles(128, 128) >= 192) return tile::launch_product<Cfg<E, 128, 128, 2, 2, 32, 4, false, false>>(A, B, K, half, epi, st, add);
+    if (tiles(256, 256) >= 192) return tile::launch_product<Cfg<E, 256, 256, 2, 4, 32, 64, 4, false, false>>(A, B, K, half, epi, st, add);
+    if (tiles(128, 128) >= 192) return tile::launch_product<Cfg<E, 128, 128, 2, 2, 32, 128, 4, false, false>>(A, B, K, half, epi, st, add);
   } else {
-    if (tiles(128, 128) >= 192) return tile::launch_product<Cfg<E, 128, 128, 2, 2, 16, 4, false, false>>(A, B, K, half, epi, st, add);
+    if (tiles(128, 128) >= 192) return tile::launch_product<Cfg<E, 128, 128, 2, 2, 16, 128, 4, false, false>>(A, B, K, half, epi, st, add);
   }
-  return tile::launch_product<Cfg<E, 64, 64, 2, 2, 16, 4, false, false>>(A, B, K, half, epi, st, add);
+  return tile::launch_product<Cfg<E, 64, 64, 2, 2, 16, 128, 4, false, false>>(A, B, K, half, epi, st, add);
 }
 
 // ---------------------------------------------------------------------------

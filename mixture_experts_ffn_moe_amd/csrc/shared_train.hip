@@ -86,16 +86,16 @@ template <bool TA, bool TB, class Epi>
 hipError_t run(const Operand& A, const Operand& B, int K, int half, const Epi& epi, uint16_t, hipStream_t st) {
   const long long M = A.count, N = Epi::PAIR ? 2ll * half : B.count;
   auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (tiles(256, 256) >= 192) return tile::launch_product<Cfg<uint16_t, 256, 256, 2, 4, 32, 2, TA, TB>>(A, B, K, half, epi, st);
-  if (tiles(128, 128) >= 192) return tile::launch_product<Cfg<uint16_t, 128, 128, 2, 2, 32, 4, TA, TB>>(A, B, K, half, epi, st);
-  return tile::launch_product<Cfg<uint16_t, 64, 64, 2, 2, 16, 4, TA, TB>>(A, B, K, half, epi, st);
+  if (tiles(256, 256) >= 192) return tile::launch_product<Cfg<uint16_t, 256, 256, 2, 4, 32, 64, 4, TA, TB>>(A, B, K, half, epi, st);
+  if (tiles(128, 128) >= 192) return tile::launch_product<Cfg<uint16_t, 128, 128, 2, 2, 32, 128, 4, TA, TB>>(A, B, K, half, epi, st);
+  return tile::launch_product<Cfg<uint16_t, 64, 64, 2, 2, 16, 128, 4, TA, TB>>(A, B, K, half, epi, st);
 }
 template <bool TA, bool TB, class Epi>
 hipError_t run(const Operand& A, const Operand& B, int K, int half, const Epi& epi, float, hipStream_t st) {
   const long long M = A.count, N = Epi::PAIR ? 2ll * half : B.count;
   auto tiles = [&](int bm, int bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-  if (tiles(128, 128) >= 192) return tile::launch_product<Cfg<float, 128, 128, 2, 2, 16, 4, TA, TB>>(A, B, K, half, epi, st);
-  return tile::launch_product<Cfg<float, 64, 64, 2, 2, 16, 4, TA, TB>>(A, B, K, half, epi, st);
+  if (tiles(128, 128) >= 192) return tile::launch_product<Cfg<float, 128, 128, 2, 2, 16, 128, 4, TA, TB>>(A, B, K, half, epi, st);
+  return tile::launch_product<Cfg<float, 64, 64, 2, 2, 16, 128, 4, TA, TB>>(A, B, K, half, epi, st);
 }
 
 template <class E>

@@ -6,8 +6,8 @@
 // Either operand is stored with k contiguous (rows of k: x, weights in the
 // forward pass) or with k as the row index ("k-rows": weights where the
 // gradient runs back through them, both operands of a weight gradient).
-//   * global -> LDS copies are direct (dma16), a ring of SLOTS k-tiles of 128
-//     bytes of k a row.  A k-contiguous tile holds 128-byte rows whose 16-byte
+//   * global -> LDS copies are direct (dma16), a ring of SLOTS k-tiles of KB
+//     bytes of k a row.  A k-contiguous tile holds KB-byte rows whose 16-byte
 //     chunks are XOR-swizzled by row; a k-rows tile holds BK rows of the
 //     tile's columns, swizzled in units of 16 columns.
 //   * operands of k-rows tiles are transposed on the way out of LDS: bf16 by
@@ -72,29 +72,34 @@ struct Operand {
   int count;  // rows m (or n), k-rows: columns
 };
 
-template <class E_, int BM_, int BN_, int WM_, int WN_, int F_, int SLOTS_, bool TA_, bool TB_>
+template <class E_, int BM_, int BN_, int WM_, int WN_, int F_, int KB_, int SLOTS_, bool TA_, bool TB_>
 struct Cfg {
   typedef E_ E;
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, F = F_, SLOTS = SLOTS_;
+  static constexpr int KB = KB_;  // bytes of k of a k-tile's row
   static constexpr bool TA = TA_, TB = TB_;  // operand stored as k-rows
   typedef Mma<E, F> M;
-  static constexpr int ES = sizeof(E), BK = 128 / ES, EPC = 16 / ES;  // elements of a 16-byte chunk
+  static constexpr int ES = sizeof(E), BK = KB / ES, EPC = 16 / ES;  // elements of a 16-byte chunk
   static constexpr int NW = WM * WN, NTHR = NW * 64;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / F, FN = TN / F;
   static constexpr int NSUB = BK / M::SUB, CPS = 64 / F;  // substeps of a k-tile, chunks of a substep
-  static constexpr int AQ = BM / 8 / NW, BQ = BN / 8 / NW;  // 1 KB copies a wave makes of a k-tile
-  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, SLOT_BYTES = A_BYTES + B_BYTES;
+  static constexpr int AQ = BM * KB / 1024 / NW, BQ = BN * KB / 1024 / NW;  // 1 KB copies a wave makes of a k-tile
+  static constexpr int A_BYTES = BM * KB, B_BYTES = BN * KB, SLOT_BYTES = A_BYTES + B_BYTES;
   static constexpr int STRIP_LD = TN + 4;  // floats
   static constexpr int STRIP_BYTES = F * STRIP_LD * 4;
   static constexpr int LDS_BYTES = SLOTS * SLOT_BYTES > NW * STRIP_BYTES ? SLOTS * SLOT_BYTES : NW * STRIP_BYTES;
-  static_assert(BM % (8 * NW) == 0 && BN % (8 * NW) == 0 && TM % F == 0 && TN % F == 0, "tile split");
+  static_assert(BM * KB % (1024 * NW) == 0 && BN * KB % (1024 * NW) == 0 && TM % F == 0 && TN % F == 0, "tile split");
   static_assert(SLOTS >= 2 && (SLOTS - 2) * (AQ + BQ) < 64, "vmcnt");
   static_assert(LDS_BYTES <= 160 * 1024, "LDS");
 };
 
 // Swizzle of a k-contiguous tile: 16 rows read together hit 16 distinct
 // 16-byte slots of the 256 bytes that LDS serves at once.
-__device__ __forceinline__ int swz_row(int row) { return (row >> 1) & 7; }
+template <int KB>
+__device__ __forceinline__ int swz_row(int row) {
+  static_assert(KB == 128 || KB == 64, "row bytes");
+  return KB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
+}
 
 // Swizzle of a k-rows tile of C columns: XOR of the 16-column unit of row k.
 // 32 lanes of a bf16 read take four rows (F = 32: of two adjacent units) or
@@ -120,8 +125,9 @@ __device__ __forceinline__ void copy_offsets(uint32_t (&off)[Q], int first, int 
   for (int i = 0; i < Q; ++i) {
     const int q = wave + C::NW * i;
     if (!KROWS) {
-      const int row = q * 8 + (lane >> 3);
-      int c = (lane & 7) ^ swz_row(row);
+      constexpr int CPR = C::KB / 16;  // chunks of a row
+      const int row = q * (64 / CPR) + lane / CPR;
+      int c = (lane % CPR) ^ swz_row<C::KB>(row);
       if (c * C::EPC >= k_left) c = 0;
       off[i] = ((uint32_t)row_of(row) * (uint32_t)ld + (uint32_t)(c * C::EPC)) * C::ES;
     } else {
@@ -142,8 +148,8 @@ __device__ __forceinline__ typename C::M::frag read_frag(const char* t, int r0, 
   typedef typename C::E E;
   if constexpr (!KROWS) {
     const int row = r0 + lane % C::F;
-    const int c = (ks * C::CPS + lane / C::F) ^ swz_row(row);
-    return *reinterpret_cast<const typename C::M::frag*>(t + row * 128 + c * 16);
+    const int c = (ks * C::CPS + lane / C::F) ^ swz_row<C::KB>(row);
+    return *reinterpret_cast<const typename C::M::frag*>(t + row * C::KB + c * 16);
   } else if constexpr (C::ES == 2) {
     const int g = lane >> 4, i = lane & 15;
     const int unit = r0 / 16 + (C::F == 32 ? (g & 1) : 0);
@@ -248,26 +254,37 @@ __device__ __forceinline__ void product(const Operand A, const Operand B, int K,
     const int up = r >= C::BN / 2;
     return up * half + min(n0 + r - up * (C::BN / 2), half - 1);
   };
-  const size_t a_step = C::TA ? (size_t)C::BK * A.ld * C::ES : (size_t)128;
-  const size_t b_step = C::TB ? (size_t)C::BK * B.ld * C::ES : (size_t)128;
+  const size_t a_step = C::TA ? (size_t)C::BK * A.ld * C::ES : (size_t)C::KB;
+  const size_t b_step = C::TB ? (size_t)C::BK * B.ld * C::ES : (size_t)C::KB;
   uint32_t aoff[C::AQ], boff[C::BQ];
   copy_offsets<C, C::TA, C::BM>(aoff, m0, A.count, A.ld, K, wave, lane, arow);
   copy_offsets<C, C::TB, C::BN>(boff, n0, B.count, B.ld, K, wave, lane, brow);
 
   const uint32_t lds = (uint32_t)(uintptr_t)smem;
-  auto issue = [&](int kt) {
-    if (kt == KT - 1 && kt > 0 && K % C::BK != 0) {  // the last k-tile is short
+  // Copies: k-tile `next` goes out piece by piece.  Past the last k-tile the
+  // last one is copied again (into slots that are not read any more), so that
+  // every wait counts the same number of copies.
+  int next = 0;
+  uint32_t slot = 0;
+  const char *pa = nullptr, *pb = nullptr;
+  auto copy_begin = [&]() {
+    const int kt = min(next, KT - 1);
+    if (kt > 0 && next == KT - 1 && K % C::BK != 0) {  // the last k-tile is short
       copy_offsets<C, C::TA, C::BM>(aoff, m0, A.count, A.ld, K - kt * C::BK, wave, lane, arow);
       copy_offsets<C, C::TB, C::BN>(boff, n0, B.count, B.ld, K - kt * C::BK, wave, lane, brow);
     }
-    const uint32_t s = lds + (uint32_t)((kt % C::SLOTS) * C::SLOT_BYTES);
-    const char* pa = uniform_ptr(a0 + kt * a_step);
-    const char* pb = uniform_ptr(b0 + kt * b_step);
-#pragma unroll
-    for (int i = 0; i < C::AQ; ++i) dma16(s + (uint32_t)(wave + C::NW * i) * 1024u, pa, aoff[i]);
-#pragma unroll
-    for (int i = 0; i < C::BQ; ++i) dma16(s + C::A_BYTES + (uint32_t)(wave + C::NW * i) * 1024u, pb, boff[i]);
+    slot = lds + (uint32_t)((next % C::SLOTS) * C::SLOT_BYTES);
+    pa = uniform_ptr(a0 + kt * a_step);
+    pb = uniform_ptr(b0 + kt * b_step);
+    ++next;
   };
+  auto copy_piece = [&](int i) {
+    if (i < C::AQ)
+      dma16(slot + (uint32_t)(wave + C::NW * i) * 1024u, pa, aoff[i]);
+    else
+      dma16(slot + C::A_BYTES + (uint32_t)(wave + C::NW * (i - C::AQ)) * 1024u, pb, boff[i - C::AQ]);
+  };
+  constexpr int NI = C::AQ + C::BQ;
 
   typename C::M::acc acc[C::FM][C::FN];
 #pragma unroll
@@ -283,44 +300,95 @@ __device__ __forceinline__ void product(const Operand A, const Operand B, int K,
   };
   static_assert(!PAIR || C::FN % 2 == 0, "gate and up fragments of a wave");
 
+  if (KT > 0) {
+    for (int s = 0; s < C::SLOTS - 1; ++s) {
+      copy_begin();
 #pragma unroll
-  for (int s = 0; s < C::SLOTS - 1; ++s)
-    if (s < KT) issue(s);
-  constexpr int LEAD = (C::SLOTS - 2) * (C::AQ + C::BQ);
-  // k-tile kt has landed, and the slot of k-tile kt - 1 is free again
-  auto advance = [&](int kt) {
-    if (kt + C::SLOTS - 2 < KT)
-      wait_vmcnt<LEAD>();
-    else
-      wait_vmcnt<0>();
+      for (int i = 0; i < NI; ++i) copy_piece(i);
+    }
+  }
+  // The next k-tile has landed for every wave, and the slot of the one before it is free.
+  auto landed = [&]() {
+    wait_vmcnt<(C::SLOTS - 2) * NI>();
     slot_barrier();
-    if (kt + C::SLOTS - 1 < KT) issue(kt + C::SLOTS - 1);
   };
-  auto substep = [&](const char* ta, int ks, auto mask) {
-    const char* tb = ta + C::A_BYTES;
-    typename C::M::frag fa[C::FM], fb[C::FN];
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i) fa[i] = mask(read_frag<C, C::TA, C::BM>(ta, wm * C::TM + C::F * i, ks, lane));
-#pragma unroll
-    for (int j = 0; j < C::FN; ++j) fb[j] = mask(read_frag<C, C::TB, C::BN>(tb, b_r0(j), ks, lane));
-#pragma unroll
-    for (int i = 0; i < C::FM; ++i)
-#pragma unroll
-      for (int j = 0; j < C::FN; ++j) acc[i][j] = C::M::mul(fb[j], fa[i], acc[i][j]);
+  struct Frags {
+    typename C::M::frag a[C::FM], b[C::FN];
   };
-  typedef typename C::M::frag Frag;
+  // Fragment q of a substep, in the order in which products need them.
+  constexpr int NF = C::FM + C::FN;
+  auto read = [&](Frags& f, int q, const char* ta, int ks) {
+    if (q >= 1 && q <= C::FN)
+      f.b[q - 1] = read_frag<C, C::TB, C::BN>(ta + C::A_BYTES, b_r0(q - 1), ks, lane);
+    else {
+      const int i = q ? q - C::FN : 0;
+      f.a[i] = read_frag<C, C::TA, C::BM>(ta, wm * C::TM + C::F * i, ks, lane);
+    }
+  };
+  auto tile_at = [&](int kt) { return smem + (kt % C::SLOTS) * C::SLOT_BYTES; };
+  // Products n0 .. n1 of a substep's FM x FN.  Behind every product goes a read
+  // of the next substep's operands (RPP of them, as long as there are any), then copies p0 .. p1,
+  // spread over the products that are left: a wave issues in order, and a
+  // run of reads or copies would fill their queue and hold up the products
+  // behind it.
+  constexpr int NP = C::FM * C::FN, RPP = (2 * NF + NP - 1) / NP;
+  auto multiply = [&](const Frags& f, int n0, int n1, Frags* into, const char* ta, int ks, int p0, int p1) {
+    const int rn = into ? (NF + RPP - 1) / RPP : 0;          // products that carry reads
+    const int cn = n1 - n0 - rn > 0 ? n1 - n0 - rn : 1;      // products that may carry copies
+#pragma unroll
+    for (int n = n0; n < n1; ++n) {
+      const int i = n / C::FN, j = n % C::FN;
+      acc[i][j] = C::M::mul(f.b[j], f.a[i], acc[i][j]);
+      if (into) {
+#pragma unroll
+        for (int q = (n - n0) * RPP; q < (n - n0 + 1) * RPP; ++q)
+          if (q < NF) read(*into, q, ta, ks);
+        if (n == n1 - 1)
+#pragma unroll
+          for (int q = (n - n0 + 1) * RPP; q < NF; ++q) read(*into, q, ta, ks);
+      }
+#pragma unroll
+      for (int p = p0; p < p1; ++p)
+        if (n1 - cn + (p - p0) * cn / (p1 - p0) == n) copy_piece(p);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // The operands of a substep are read while the one before it multiplies; the
+  // last substep of a k-tile has a quarter of its products issued before the
+  // wait for the next k-tile.  A k-tile's copies lie between the products of
+  // the k-tile SLOTS - 1 before it.
   const int KF = K / C::BK;
-  for (int kt = 0; kt < KF; ++kt) {
-    advance(kt);
+  static_assert(C::NSUB % 2 == 0 && NP % 4 == 0, "substeps in pairs");
+  Frags f[2];
+  if (KF > 0) {
+    landed();
 #pragma unroll
-    for (int ks = 0; ks < C::NSUB; ++ks) substep(smem + (kt % C::SLOTS) * C::SLOT_BYTES, ks, [](Frag f) { return f; });
+    for (int q = 0; q < NF; ++q) read(f[0], q, tile_at(0), 0);
+    for (int kt = 0; kt < KF; ++kt) {
+      copy_begin();
+      const char* ta = tile_at(kt);
+#pragma unroll
+      for (int ks = 0; ks + 1 < C::NSUB; ++ks)
+        multiply(f[ks & 1], 0, NP, &f[(ks + 1) & 1], ta, ks + 1, NI * ks / (C::NSUB - 1), NI * (ks + 1) / (C::NSUB - 1));
+      multiply(f[1], 0, NP / 4, nullptr, nullptr, 0, 0, 0);
+      landed();
+      // past the last whole k-tile the reads fetch what is in the ring and nothing uses it
+      multiply(f[1], NP / 4, NP, &f[0], tile_at(kt + 1), 0, 0, 0);
+    }
   }
   if (KF < KT) {
-    advance(KF);
+    if (KF == 0) landed();
     const int left = K - KF * C::BK;
-    for (int ks = 0; ks * C::M::SUB < left; ++ks)
-      substep(smem + (KF % C::SLOTS) * C::SLOT_BYTES, ks,
-              [&](Frag f) { return mask_k<C>(f, left - ks * C::M::SUB, lane); });
+    for (int ks = 0; ks * C::M::SUB < left; ++ks) {
+      Frags& t = f[0];
+#pragma unroll
+      for (int q = 0; q < NF; ++q) read(t, q, tile_at(KF), ks);
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) t.a[i] = mask_k<C>(t.a[i], left - ks * C::M::SUB, lane);
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j) t.b[j] = mask_k<C>(t.b[j], left - ks * C::M::SUB, lane);
+      multiply(t, 0, NP, nullptr, nullptr, 0, 0, 0);
+    }
   }
   if constexpr (Extra::ON) extra.template add<C>(acc, m0 + wm * C::TM, [&](int j) {
     const int r = b_r0(j) + lane % C::F;
@@ -330,6 +398,7 @@ __device__ __forceinline__ void product(const Operand A, const Operand B, int K,
   }, lane);
 
   settle();
+  wait_vmcnt<0>();  // copies that nothing waited for
   __syncthreads();  // every wave is past its last LDS read: the ring is free
   float* strip = reinterpret_cast<float*>(smem + wave * C::STRIP_BYTES);
   constexpr int WC = PAIR ? C::TN / 2 : C::TN;  // output columns of the wave

@@ -32,19 +32,17 @@ constexpr int kMaxParts = 8;
 bool small_path(const Ffn& f) { return f.bf16 && f.T <= kSmallTokens; }
 
 // Parts of K whose low-rank sums are kept apart, so that few tokens still
-// spread over the chip: 256 workgroups, at least 256 columns a part.
+// spread over the chip: 512 workgroups, at least 512 columns a part.
 int parts_of(const Ffn& f, int K) {
-  const int units = small_path(f) ? f.T : (f.T + 31) / 32;
-  int p = 256 / units;
-  p = p < K / 256 ? p : K / 256;
+  const int units = small_path(f) ? 1 : (f.T + 31) / 32;
+  int p = 512 / units;
+  p = p < K / 512 ? p : K / 512;
   return p < 1 ? 1 : p > kMaxParts ? kMaxParts : p;
 }
 
-constexpr int kPlanThreads = 1024;
-int plan_blocks(int T) {
-  const int b = (T + 8191) / 8192;
-  return b < 256 ? b : 256;
-}
+// Tokens of a workgroup of the sort.
+constexpr int kPlanThreads = 1024, kPlanChunk = 8192;
+int plan_blocks(int T) { return (T + kPlanChunk - 1) / kPlanChunk; }
 
 struct Space {
   int32_t *perm, *sorted, *first, *hist;
@@ -108,25 +106,44 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count(const int32_t* ids, i
 }
 
 // Every workgroup finds its first position in every bin from all counts, then
-// places its chunk.  Block 0 writes the bins' first positions.
+// places its chunk.  Block 0 writes the bins' first positions.  A lone
+// workgroup (blocks == 1) counts by itself and reads no hist.
 __global__ __launch_bounds__(kPlanThreads) void plan_place(const int32_t* ids, int T, int L, int chunk,
                                                            const int32_t* hist, int blocks, int32_t* perm,
                                                            int32_t* sorted, int32_t* first) {
   __shared__ int start[kLoraMaxAdapters + 1];
   __shared__ int wave_sum[kPlanThreads / 64];
   __shared__ int carry;
-  if (threadIdx.x == 0) carry = 0;
+  constexpr int KEEP = kPlanChunk / kPlanThreads;  // a thread's tokens of a chunk
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t0 = blockIdx.x * chunk, t1 = min(T, t0 + chunk);
+  int bins[KEEP];
+#pragma unroll
+  for (int q = 0; q < KEEP; ++q) {
+    const int t = t0 + q * kPlanThreads + threadIdx.x;
+    bins[q] = t < t1 ? bin_of(ids[t], L) : -1;
+  }
+  if (threadIdx.x == 0) carry = 0;
+  if (blocks == 1) {
+    for (int i = threadIdx.x; i <= L; i += kPlanThreads) start[i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < KEEP; ++q) count_up(start, bins[q], bins[q] >= 0);
+  }
   __syncthreads();
   for (int i0 = 0; i0 <= L; i0 += kPlanThreads) {
     const int i = i0 + threadIdx.x;
     int total = 0, before = 0;
-    if (i <= L)
-      for (int b = 0; b < blocks; ++b) {
-        const int n = hist[(size_t)b * (L + 1) + i];
-        total += n;
-        before += b < (int)blockIdx.x ? n : 0;
-      }
+    if (i <= L) {
+      if (blocks == 1)
+        total = start[i];
+      else
+        for (int b = 0; b < blocks; ++b) {
+          const int n = hist[(size_t)b * (L + 1) + i];
+          total += n;
+          before += b < (int)blockIdx.x ? n : 0;
+        }
+    }
     int incl = total;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -146,124 +163,81 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place(const int32_t* ids, i
     __syncthreads();
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) first[L + 1] = T;
-  const int t0 = blockIdx.x * chunk, t1 = min(T, t0 + chunk);
-  for (int t = t0 + threadIdx.x; t - (int)threadIdx.x < t1; t += kPlanThreads) {
-    const bool on = t < t1;
-    const int bin = on ? bin_of(ids[t], L) : 0;
-    const int at = count_up(start, bin, on);
-    if (on) {
-      perm[at] = t;
-      sorted[at] = bin;
+#pragma unroll
+  for (int q = 0; q < KEEP; ++q) {
+    const int at = count_up(start, bins[q], bins[q] >= 0);
+    if (bins[q] >= 0) {
+      perm[at] = t0 + q * kPlanThreads + threadIdx.x;
+      sorted[at] = bins[q];
     }
   }
 }
 
 // ---------------------------------------------------------------------------
-// Shrink: 32 tokens of one adapter, RB * 32 ranks, a part of K split over
-// the waves.
+// Shrink: 32 tokens of one adapter, BN ranks, a part of K.  Operand fragments
+// read straight from memory would touch 16 rows per 16 lanes (eight times the
+// line accesses of whole rows: 27 us for 8192 tokens, K = 2048, rank 64), so the rows
+// come through LDS like those of any tiled product.
 
-constexpr int kShrinkWaves = 4;
+struct Gather {
+  static constexpr bool ON = false, MAPPED = true;
+  const int32_t* perm;
+  __device__ __forceinline__ int a_row(int p) const { return perm[p]; }
+  __device__ __forceinline__ int out_row(int p) const { return p; }
+};
+struct StoreLow {
+  static constexpr bool PAIR = false;
+  float* v;
+  int r;
+  float scale;
+  struct Pre {};
+  __device__ __forceinline__ Pre load(int, int) const { return Pre{}; }
+  __device__ __forceinline__ void store(int row, int col, f32x4* s, const Pre&) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] *= scale;
+    tile::store8(v + (size_t)row * r + col, s[0], s[1]);
+  }
+};
 
-template <class E, int RB>
-__global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(const E* x, const E* a, const float* scale,
-                                                                   const int32_t* perm, const int32_t* first, int T,
-                                                                   int K, int L, int r, int parts, float* v) {
-  constexpr int F = sizeof(E) == 2 ? 32 : 16, FT = 32 / F, FR = RB * 32 / F, EPC = 16 / sizeof(E);
-  typedef Mma<E, F> M;
-  constexpr int LD = RB * 32 + 4;
-  __shared__ float sum[kShrinkWaves][32 * LD];
-  __shared__ int found[3];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+template <class C>
+__global__ __launch_bounds__(C::NTHR) void shrink_kernel(const typename C::E* x, const typename C::E* a,
+                                                         const float* scale, const int32_t* perm,
+                                                         const int32_t* first, int T, int K, int L, int r, int parts,
+                                                         float* v) {
+  __shared__ __attribute__((aligned(1024))) char smem[C::LDS_BYTES];
   // unit -> (adapter, first position): the units of an adapter with n tokens
-  // are ceil(n / 32), adapters in order; wave 0 walks 64 of them at a time
-  if (wave == 0) {
-    int u = blockIdx.x, got = 0, ad = 0, p0 = 0, p1 = 0;
-    for (int i0 = 0; i0 < L && !got; i0 += 64) {
-      const int i = i0 + lane;
-      const int lo = i < L ? first[i] : 0, hi = i < L ? first[i + 1] : 0;
-      int incl = (hi - lo + 31) / 32;
-      const int mine = incl;
+  // are ceil(n / BM), adapters in order; every wave walks 64 of them at a time
+  const int lane = threadIdx.x & 63;
+  int u = blockIdx.x, ad = -1, p0 = 0, p1 = 0;
+  for (int i0 = 0; i0 < L; i0 += 64) {
+    const int i = i0 + lane;
+    const int lo = i < L ? first[i] : 0, hi = i < L ? first[i + 1] : 0;
+    const int mine = (hi - lo + C::BM - 1) / C::BM;
+    int incl = mine;
 #pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_up(incl, d);
-        if (lane >= d) incl += o;
-      }
-      const uint64_t hit = __ballot(incl > u);
-      if (hit) {
-        const int w = __ffsll((long long)hit) - 1;
-        ad = i0 + w;
-        const int off = (u - __shfl(incl - mine, w)) * 32;
-        p0 = __shfl(lo, w) + off;
-        p1 = min(p0 + 32, __shfl(hi, w));
-        got = 1;
-      } else {
-        u -= __shfl(incl, 63);
-      }
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(incl, d);
+      if (lane >= d) incl += o;
     }
-    if (lane == 0) {
-      found[0] = got ? ad : -1;
-      found[1] = p0;
-      found[2] = p1;
+    const uint64_t hit = __ballot(incl > u);
+    if (hit) {
+      const int w = __ffsll((long long)hit) - 1;
+      ad = i0 + w;
+      p0 = __shfl(lo, w) + (u - __shfl(incl - mine, w)) * C::BM;
+      p1 = __shfl(hi, w);
+      break;
     }
+    u -= __shfl(incl, 63);
   }
-  __syncthreads();
-  const int ad = found[0], p0 = found[1], p1 = found[2];
+  ad = __builtin_amdgcn_readfirstlane(ad);
+  p0 = __builtin_amdgcn_readfirstlane(p0);
+  p1 = min(__builtin_amdgcn_readfirstlane(p1), p0 + C::BM);
   if (ad < 0) return;
-  const int steps = K / M::SUB, part = blockIdx.y;
-  const int s0 = (int)((long long)steps * part / parts), s1 = (int)((long long)steps * (part + 1) / parts);
-  const int k0 = s0 + (s1 - s0) * wave / kShrinkWaves, k1 = s0 + (s1 - s0) * (wave + 1) / kShrinkWaves;
-  const E *px[FT], *pa[FR];
-#pragma unroll
-  for (int i = 0; i < FT; ++i)
-    px[i] = x + (size_t)perm[min(p0 + F * i + lane % F, p1 - 1)] * K + (lane / F) * EPC;
-#pragma unroll
-  for (int j = 0; j < FR; ++j)
-    pa[j] = a + ((size_t)ad * r + min(F * j + lane % F, r - 1)) * K + (lane / F) * EPC;
-  typename M::acc acc[FT][FR];
-#pragma unroll
-  for (int i = 0; i < FT; ++i)
-#pragma unroll
-    for (int j = 0; j < FR; ++j)
-#pragma unroll
-      for (int e = 0; e < F * F / 64; ++e) acc[i][j][e] = 0.0f;
-#pragma unroll 4
-  for (int s = k0; s < k1; ++s) {
-    typename M::frag fx[FT], fa[FR];
-#pragma unroll
-    for (int i = 0; i < FT; ++i) fx[i] = *reinterpret_cast<const typename M::frag*>(px[i] + (size_t)s * M::SUB);
-#pragma unroll
-    for (int j = 0; j < FR; ++j) fa[j] = *reinterpret_cast<const typename M::frag*>(pa[j] + (size_t)s * M::SUB);
-#pragma unroll
-    for (int i = 0; i < FT; ++i)
-#pragma unroll
-      for (int j = 0; j < FR; ++j) acc[i][j] = M::mul(fa[j], fx[i], acc[i][j]);
-  }
-  tile::settle();
-#pragma unroll
-  for (int i = 0; i < FT; ++i)
-#pragma unroll
-    for (int j = 0; j < FR; ++j)
-#pragma unroll
-      for (int q = 0; q < F * F / 256; ++q) {
-        const f32x4 t = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        *reinterpret_cast<f32x4*>(&sum[wave][(F * i + lane % F) * LD + F * j + 8 * q + 4 * (lane / F)]) = t;
-      }
-  __syncthreads();
-  const float sc = scale[ad];
-  for (int i = tid; i < 32 * (r / 4); i += kShrinkWaves * 64) {
-    const int row = i / (r / 4), c = (i % (r / 4)) * 4;
-    if (p0 + row >= p1) break;
-    f32x4 t = *reinterpret_cast<const f32x4*>(&sum[0][row * LD + c]);
-#pragma unroll
-    for (int w = 1; w < kShrinkWaves; ++w) {
-      const f32x4 o = *reinterpret_cast<const f32x4*>(&sum[w][row * LD + c]);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) t[e] += o[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) t[e] *= sc;
-    *reinterpret_cast<f32x4*>(v + ((size_t)part * T + p0 + row) * r + c) = t;
-  }
+  const int part = blockIdx.y, tiles = (K + C::BK - 1) / C::BK;
+  const int k0 = tiles * part / parts * C::BK, k1 = min(K, tiles * (part + 1) / parts * C::BK);
+  const StoreLow epi{v + (size_t)part * T * r, r, scale[ad]};
+  tile::product<C, StoreLow, Gather>(Operand{x + k0, K, p1}, Operand{a + (size_t)ad * r * K + k0, K, r}, k1 - k0, 0, p0,
+                                     blockIdx.z * C::BN, epi, Gather{perm}, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -271,7 +245,7 @@ __global__ __launch_bounds__(kShrinkWaves * 64) void shrink_kernel(const E* x, c
 
 template <class E>
 struct AddLora {
-  static constexpr bool ON = true;
+  static constexpr bool ON = true, MAPPED = true;
   const int32_t *perm, *sorted;
   const float* v;  // [parts, T, r]
   const E* b;      // [L, rows, r]
@@ -308,38 +282,50 @@ struct AddLora {
   // m: the wave's first position; brow(j): this lane's row of b in fragment j.
   template <class C, class Row>
   __device__ __forceinline__ void add(typename C::M::acc (&acc)[C::FM][C::FN], int m, Row brow, int lane) const {
-    constexpr int EPC = C::EPC;
-    const int kl = (lane / C::F) * EPC;
+    constexpr int KS = 4;  // matrix steps whose low-rank values a lane holds at a time
+    const int kl = (lane / C::F) * C::EPC;
+    const E* pb[C::FN];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j) pb[j] = b + (size_t)brow(j) * r + kl;
 #pragma unroll
     for (int i = 0; i < C::FM; ++i) {
       const int p = min(m + C::F * i + lane % C::F, T - 1);
       const int mine = sorted[p];
-      int cur = __builtin_amdgcn_readfirstlane(mine);
-      while (cur < L) {
-        typename C::M::acc d[C::FN];
+      const int lead = __builtin_amdgcn_readfirstlane(mine);
+      if (lead >= L) continue;
+      for (int k0 = 0; k0 < r; k0 += KS * C::M::SUB) {
+        typename C::M::frag fv[KS];
 #pragma unroll
-        for (int j = 0; j < C::FN; ++j)
+        for (int k = 0; k < KS; ++k) fv[k] = values(p, k0 + k * C::M::SUB + kl);
+        int cur = lead;
+        while (cur < L) {
+          typename C::M::acc d[C::FN];
 #pragma unroll
-          for (int e = 0; e < C::F * C::F / 64; ++e) d[j][e] = 0.0f;
-        for (int k = 0; k < r; k += C::M::SUB) {
-          const typename C::M::frag fv = values(p, k + kl);
+          for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-          for (int j = 0; j < C::FN; ++j) {
-            typename C::M::frag fb = {};
-            if (k + kl < r)
-              fb = *reinterpret_cast<const typename C::M::frag*>(b + ((size_t)cur * rows + brow(j)) * r + k + kl);
-            d[j] = C::M::mul(fb, fv, d[j]);
+            for (int e = 0; e < C::F * C::F / 64; ++e) d[j][e] = 0.0f;
+          const size_t at = (size_t)cur * rows * r + k0;
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            if (k0 + k * C::M::SUB >= r) break;
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) {
+              typename C::M::frag fb = {};
+              if (k0 + k * C::M::SUB + kl < r)
+                fb = *reinterpret_cast<const typename C::M::frag*>(pb[j] + at + k * C::M::SUB);
+              d[j] = C::M::mul(fb, fv[k], d[j]);
+            }
           }
+          tile::settle();
+          // every lane holds one row: it takes the product of its own adapter
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+            for (int e = 0; e < C::F * C::F / 64; ++e) acc[i][j][e] = mine == cur ? acc[i][j][e] + d[j][e] : acc[i][j][e];
+          const uint64_t later = __ballot(mine > cur);
+          if (later == 0) break;
+          cur = __builtin_amdgcn_readlane(mine, __ffsll((long long)later) - 1);
         }
-        tile::settle();
-        // every lane holds one row: it takes the product of its own adapter
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-          for (int e = 0; e < C::F * C::F / 64; ++e) acc[i][j][e] = mine == cur ? acc[i][j][e] + d[j][e] : acc[i][j][e];
-        const uint64_t later = __ballot(mine > cur);
-        if (later == 0) break;
-        cur = __builtin_amdgcn_readlane(mine, __ffsll((long long)later) - 1);
       }
     }
   }
@@ -366,15 +352,15 @@ hipError_t big(const Ffn& f, const Lora& l, const void* x, int K, const void* w,
   const Space s = space(f, l, ws);
   const int parts = parts_of(f, K);
   const int units = (f.T + 31) / 32 + (l.L < f.T ? l.L : f.T);
-  const dim3 grid(units, parts), blk(kShrinkWaves * 64);
-#define SHRINK(RB)                                                                                                 \
-  hipLaunchKernelGGL((shrink_kernel<E, RB>), grid, blk, 0, st, (const E*)x, (const E*)a, scale, s.perm, s.first, \
-                     f.T, K, l.L, l.r, parts, s.v)
-  if (l.r <= 32) SHRINK(1);
-  else if (l.r <= 64) SHRINK(2);
-  else SHRINK(4);
-#undef SHRINK
-  const hipError_t e = hipGetLastError();
+  auto shrink = [&](auto cfg) {
+    typedef decltype(cfg) C;
+    static_assert(C::BM == 32, "units of 32 tokens");
+    hipLaunchKernelGGL(shrink_kernel<C>, dim3(units, parts, (l.r + C::BN - 1) / C::BN), dim3(C::NTHR), 0, st,
+                       (const E*)x, (const E*)a, scale, s.perm, s.first, f.T, K, l.L, l.r, parts, s.v);
+    return hipGetLastError();
+  };
+  const hipError_t e = l.r <= 32 ? shrink(Cfg<E, 32, 32, 1, 2, 16, 128, 4, false, false>{})
+                                 : shrink(Cfg<E, 32, 64, 1, 4, 16, 128, 4, false, false>{});
   if (e != hipSuccess) return e;
   const AddLora<E> add{s.perm, s.sorted, s.v, (const E*)b, f.T, l.L, l.r, rows, parts};
   const Operand A{x, K, f.T}, B{w, K, rows};
@@ -392,88 +378,156 @@ hipError_t big(const Ffn& f, const Lora& l, const void* x, int K, const void* w,
 // ---------------------------------------------------------------------------
 // Up to kSmallTokens tokens.
 
-// v[part, t, j] = s_a A_a[j] . x[t] over a part of K: one workgroup a (token,
-// part), a wave the ranks wave, wave + 4, ...
+// v[part, t, j] = s_a A_a[j] . x[t] over a part of K, a wave for each.
 __global__ __launch_bounds__(256) void shrink_small(const uint16_t* x, const uint16_t* a, const float* scale,
                                                     const int32_t* ids, int T, int K, int L, int r, int parts,
                                                     float* v) {
-  const int t = blockIdx.x, part = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int t = blockIdx.x, part = blockIdx.y, lane = threadIdx.x & 63;
+  const int j = blockIdx.z * 4 + (threadIdx.x >> 6);  // r is a multiple of 8
   const int ad = ids[t];
   if (ad < 0 || ad >= L) return;
   const int chunks = K / 8;
-  const int c0 = (int)((long long)chunks * part / parts), c1 = (int)((long long)chunks * (part + 1) / parts);
+  const int c0 = chunks * part / parts, c1 = chunks * (part + 1) / parts;
   const float sc = scale[ad];
-  for (int j = wave; j < r; j += 4) {
-    float s = 0.0f;
-    for (int c = c0 + lane; c < c1; c += 64) {
-      tile::Vec8<uint16_t> p, q;
-      p.load(x + (size_t)t * K + c * 8);
-      q.load(a + ((size_t)ad * r + j) * K + c * 8);
+  float s = 0.0f;
+  for (int c = c0 + lane; c < c1; c += 64) {
+    tile::Vec8<uint16_t> p, q;
+    p.load(x + (size_t)t * K + c * 8);
+    q.load(a + ((size_t)ad * r + j) * K + c * 8);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(p[e], q[e], s);
-    }
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-    if (lane == 0) v[((size_t)part * T + t) * r + j] = s * sc;
+    for (int e = 0; e < 8; ++e) s = fmaf(p[e], q[e], s);
   }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  if (lane == 0) v[((size_t)part * T + t) * r + j] = s * sc;
 }
 
-// 16 rows of W (PAIR: 8 gate rows and their up rows), all tokens: the waves
-// split K, their sums meet in LDS, and a thread finishes one (token, column).
-template <bool PAIR>
-__global__ __launch_bounds__(1024) void stream_kernel(const uint16_t* x, const uint16_t* w, const uint16_t* b,
-                                                      const int32_t* ids, const float* v, const uint16_t* residual,
-                                                      uint16_t* out, int T, int K, int N, int L, int r, int parts) {
-  extern __shared__ float smem[];  // [waves][16][20] sums, then [16][r] low-rank values
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, nw = blockDim.x >> 6;
-  const int half = N / 2;
-  const int n0 = blockIdx.x * (PAIR ? 8 : 16);
-  auto wrow = [&](int i) { return PAIR ? (i < 8 ? n0 + i : half + n0 + i - 8) : n0 + i; };
-  const uint16_t* pw = w + (size_t)wrow(lane & 15) * K + (lane >> 4) * 8;
-  const uint16_t* px = x + (size_t)min(lane & 15, T - 1) * K + (lane >> 4) * 8;
-  const int steps = K / 32;
-  const int k0 = steps * wave / nw, k1 = steps * (wave + 1) / nw;
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-  for (int s = k0; s < k1; ++s) {
-    const bf16x8 fw = *reinterpret_cast<const bf16x8*>(pw + (size_t)s * 32);
-    const bf16x8 fx = *reinterpret_cast<const bf16x8*>(px + (size_t)s * 32);
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw, fx, acc, 0, 0, 0);
-  }
-  tile::settle();
-  // lane: token lane % 16, rows 4 * (lane / 16) + e
-  *reinterpret_cast<f32x4*>(smem + (wave * 16 + (lane & 15)) * 20 + 4 * (lane >> 4)) = acc;
-  float* low = smem + nw * 16 * 20;
-  for (int i = tid; i < T * r; i += blockDim.x) {
-    const int ad = ids[i / r];
-    float s = 0.0f;
-    if (ad >= 0 && ad < L)
-      for (int p = 0; p < parts; ++p) s += v[(size_t)p * T * r + i];
-    low[i] = s;
-  }
-  __syncthreads();
-  if (tid >= 256) return;
-  const int t = tid >> 4, i = tid & 15;  // token, row of the sixteen
-  float s = 0.0f;
-  if (t < T) {
-    for (int q = 0; q < nw; ++q) s += smem[(q * 16 + t) * 20 + i];
-    const int ad = ids[t];
-    if (ad >= 0 && ad < L) {
-      const uint16_t* pb = b + ((size_t)ad * N + wrow(i)) * r;
-      float d = 0.0f;
-      for (int k = 0; k < r; k += 8) {
-        tile::Vec8<uint16_t> q;
-        q.load(pb + k);
+// ROWS rows of W (PAIR: half of them gate rows, then their up rows), all
+// tokens: the waves split K in chunks of 64 columns, each with a ring of its
+// own in LDS that direct copies fill with whole 128-byte rows (no workgroup
+// barrier); their sums meet in LDS, and a thread finishes one (token, row).
+// What the end needs (low-rank values, the first 32 ranks of B) is loaded right
+// behind the first copies, so that the latencies overlap.
+constexpr int kStreamWaves = 16, kStreamRing = 2;
+
+template <bool PAIR, int ROWS>
+__global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(const uint16_t* x, const uint16_t* w,
+                                                                   const uint16_t* b, const int32_t* ids,
+                                                                   const float* v, const uint16_t* residual,
+                                                                   uint16_t* out, int T, int K, int N, int L, int r,
+                                                                   int parts) {
+  static_assert(ROWS == 8 || ROWS == 16, "rows of W");
+  constexpr int SLOT = (ROWS + 16) * 128, COPIES = ROWS / 8 + 2;
+  constexpr int RING = kStreamWaves * kStreamRing * SLOT;
+  __shared__ __attribute__((aligned(1024))) char ring[RING];
+  __shared__ float low[kSmallTokens * kLoraMaxRank];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int half = N / 2, cols = PAIR ? ROWS / 2 : ROWS;
+  const int n0 = blockIdx.x * cols;
+  auto wrow = [&](int i) { return i < cols ? n0 + i : half + n0 + i - cols; };
+  const int chunks = (K + 63) / 64;
+  const uint32_t lds = (uint32_t)(uintptr_t)ring + (uint32_t)(wave * kStreamRing * SLOT);
+  uint32_t woff[ROWS / 8], xoff[2];
+  const int lr = lane >> 3;
+  int col[2];  // columns of this lane's 16 bytes, by row group
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d = fmaf(q[e], low[t * r + k + e], d);
-      }
-      s += d;
+  for (int g = 0; g < 2; ++g) {
+    const int row = g * 8 + lr;
+    col[g] = ((lane & 7) ^ tile::swz_row<128>(row)) * 8;
+    if (g < ROWS / 8) woff[g] = ((uint32_t)wrow(row) * (uint32_t)K + (uint32_t)col[g]) * 2u;
+    xoff[g] = ((uint32_t)min(row, T - 1) * (uint32_t)K + (uint32_t)col[g]) * 2u;
+  }
+  // Copies of chunk c into slot c's place; the last chunk may hold 32 columns
+  // only: what lies past them is read from the chunk's start and not used.
+  auto copy = [&](int n) {
+    const int c = wave + kStreamWaves * n;
+    const bool past = c * 64 + 64 > K;
+    const uint32_t s = lds + (uint32_t)((n % kStreamRing) * SLOT);
+    const char* pw = uniform_ptr((const char*)w + (size_t)c * 128);
+    const char* px = uniform_ptr((const char*)x + (size_t)c * 128);
+#pragma unroll
+    for (int g = 0; g < ROWS / 8; ++g) dma16(s + g * 1024u, pw, past && col[g] >= 32 ? woff[g] - col[g] * 2u : woff[g]);
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      dma16(s + ROWS * 128u + g * 1024u, px, past && col[g] >= 32 ? xoff[g] - col[g] * 2u : xoff[g]);
+  };
+  const int mine = wave < chunks ? (chunks - wave + kStreamWaves - 1) / kStreamWaves : 0;
+#pragma unroll
+  for (int n = 0; n < kStreamRing; ++n)
+    if (n < mine) copy(n);
+
+  const int t = tid / ROWS, i = tid % ROWS;  // token and row that this thread finishes
+  const bool live = t < T;
+  const int ad = live ? ids[t] : -1;
+  const bool has = ad >= 0 && ad < L;
+  const uint16_t* pb = b + ((size_t)(has ? ad : 0) * N + wrow(i)) * r;
+  tile::Vec8<uint16_t> q[4];
+  if (has) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c * 8 < r) q[c].load(pb + c * 8);
+  }
+  for (int e = tid; e < T * r; e += kStreamWaves * 64) {
+    const int a = ids[e / r];
+    float s = 0.0f;
+    if (a >= 0 && a < L)
+      for (int p = 0; p < parts; ++p) s += v[(size_t)p * T * r + e];
+    low[e] = s;
+  }
+
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  const int fr = lane & 15;
+  for (int n = 0; n < mine; ++n) {
+    // chunk n has landed; behind it at most one chunk's copies are in flight
+    if (n + 1 < mine && n > 0)
+      wait_vmcnt<COPIES>();
+    else
+      wait_vmcnt<0>();
+    __builtin_amdgcn_sched_barrier(0);
+    const char* s = ring + wave * kStreamRing * SLOT + (n % kStreamRing) * SLOT;
+    const int steps = min(2, (K - (wave + kStreamWaves * n) * 64) / 32);
+    for (int ks = 0; ks < steps; ++ks) {
+      const int c = ((ks * 4 + (lane >> 4)) ^ tile::swz_row<128>(fr)) * 16;
+      const int wr = fr % ROWS, cw = ((ks * 4 + (lane >> 4)) ^ tile::swz_row<128>(wr)) * 16;
+      const bf16x8 fw = *reinterpret_cast<const bf16x8*>(s + wr * 128 + cw);
+      const bf16x8 fx = *reinterpret_cast<const bf16x8*>(s + ROWS * 128 + fr * 128 + c);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw, fx, acc, 0, 0, 0);
+    }
+    if (n + kStreamRing < mine) {
+      __builtin_amdgcn_s_waitcnt(0xF | (7 << 4) | (0 << 8) | (3 << 14));  // the slot's reads are done
+      __builtin_amdgcn_sched_barrier(0);
+      copy(n + kStreamRing);
     }
   }
+  tile::settle();
+  __syncthreads();  // every wave is past its ring
+  // lane: token lane % 16, rows 4 * (lane / 16) + e
+  float* sums = reinterpret_cast<float*>(ring);
+  static_assert(kStreamWaves * 16 * 20 * 4 <= RING, "sums in the ring's place");
+  *reinterpret_cast<f32x4*>(sums + (wave * 16 + fr) * 20 + 4 * (lane >> 4)) = acc;
+  __syncthreads();
+  if (tid >= 16 * ROWS) return;
+  float s = 0.0f;
+  if (live)
+    for (int p = 0; p < kStreamWaves; ++p) s += sums[(p * 16 + t) * 20 + i];
+  if (has) {
+    float d = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c * 8 < r)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) d = fmaf(q[c][e], low[t * r + c * 8 + e], d);
+    for (int k = 32; k < r; k += 8) {
+      q[0].load(pb + k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) d = fmaf(q[0][e], low[t * r + k + e], d);
+    }
+    s += d;
+  }
   if (PAIR) {
-    const float up = __shfl_xor(s, 8);
-    if (t < T && i < 8) out[(size_t)t * half + n0 + i] = float_to_bf16_bits(silu_f32(s) * up);
-  } else if (t < T) {
+    const float up = __shfl_xor(s, ROWS / 2);
+    if (live && i < cols) out[(size_t)t * half + n0 + i] = float_to_bf16_bits(silu_f32(s) * up);
+  } else if (live) {
     if (residual) s += bf16_bits_to_float(residual[(size_t)t * N + n0 + i]);
     out[(size_t)t * N + n0 + i] = float_to_bf16_bits(s);
   }
@@ -485,16 +539,18 @@ hipError_t small(const Ffn& f, const Lora& l, const void* x, int K, const void* 
                  hipStream_t st) {
   const Space s = space(f, l, ws);
   const int parts = parts_of(f, K);
-  hipLaunchKernelGGL(shrink_small, dim3(f.T, parts), dim3(256), 0, st, (const uint16_t*)x, (const uint16_t*)a, scale,
-                     ids, f.T, K, l.L, l.r, parts, s.v);
-  hipError_t e = hipGetLastError();
+  hipLaunchKernelGGL(shrink_small, dim3(f.T, parts, l.r / 4), dim3(256), 0, st, (const uint16_t*)x,
+                     (const uint16_t*)a, scale, ids, f.T, K, l.L, l.r, parts, s.v);
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int steps = K / 32, nw = steps >= 64 ? 16 : steps >= 16 ? 8 : 4;
-  const int lds = (nw * 16 * 20 + f.T * l.r) * 4;
-  hipLaunchKernelGGL((stream_kernel<PAIR>), dim3(rows / 16), dim3(nw * 64), lds, st, (const uint16_t*)x,
-                     (const uint16_t*)w, (const uint16_t*)b, ids, s.v, (const uint16_t*)residual, (uint16_t*)out,
-                     f.T, K, rows, l.L, l.r, parts);
-  return hipGetLastError();
+  auto stream = [&](auto kernel, int per) {
+    hipLaunchKernelGGL(kernel, dim3(rows / per), dim3(kStreamWaves * 64), 0, st, (const uint16_t*)x,
+                       (const uint16_t*)w, (const uint16_t*)b, ids, s.v, (const uint16_t*)residual, (uint16_t*)out,
+                       f.T, K, rows, l.L, l.r, parts);
+    return hipGetLastError();
+  };
+  // sixteen rows a workgroup leave CUs without one below 4096 rows
+  return rows < 4096 ? stream(stream_kernel<PAIR, 8>, 8) : stream(stream_kernel<PAIR, 16>, 16);
 }
 
 }  // namespace
@@ -505,7 +561,11 @@ hipError_t launch_lora_plan(const Ffn& f, const Lora& l, const int32_t* ids, voi
   if (small_path(f)) return hipSuccess;
   const Space s = space(f, l, ws);
   const int blocks = plan_blocks(f.T), chunk = (f.T + blocks - 1) / blocks;
-  hipLaunchKernelGGL(plan_count, dim3(blocks), dim3(kPlanThreads), 0, st, ids, f.T, l.L, chunk, s.hist);
+  if (blocks > 1) {
+    hipLaunchKernelGGL(plan_count, dim3(blocks), dim3(kPlanThreads), 0, st, ids, f.T, l.L, chunk, s.hist);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(plan_place, dim3(blocks), dim3(kPlanThreads), 0, st, ids, f.T, l.L, chunk, s.hist, blocks,
                      s.perm, s.sorted, s.first);
   return hipGetLastError();

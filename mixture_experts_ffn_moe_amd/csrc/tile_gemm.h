@@ -222,27 +222,26 @@ struct Identity {
 
 // No low-rank addition.
 struct NoExtra {
-  static constexpr bool ON = false;
+  static constexpr bool ON = false, MAPPED = false;
   __device__ __forceinline__ int a_row(int r) const { return r; }
   __device__ __forceinline__ int out_row(int r) const { return r; }
 };
 
-// One product.  PAIR: B has two halves of `half` rows (gate, up) and a tile
-// takes BN / 2 columns of each; the epilogue then gets both values of a column.
+// One tile, from row m0 and column n0 on.  PAIR: B has two halves of `half`
+// rows (gate, up) and a tile takes BN / 2 columns of each; the epilogue then
+// gets both values of a column.
 template <class C, class Epi, class Extra>
-__device__ __forceinline__ void product(const Operand A, const Operand B, int K, int half, int tm, int tn,
+__device__ __forceinline__ void product(const Operand A, const Operand B, int K, int half, int m0, int n0,
                                         const Epi& epi, const Extra& extra, char* smem) {
   constexpr bool PAIR = Epi::PAIR;
-  constexpr int OC = PAIR ? C::BN / 2 : C::BN;  // output columns of a tile
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / C::WN, wn = wave % C::WN;
-  const int m0 = tm * C::BM, n0 = tn * OC;
   const int N = PAIR ? half : B.count;
   const int KT = (K + C::BK - 1) / C::BK;
 
   // bases of the tile (k-tile 0) and the row maps below them
-  const bool rowmap = Extra::ON;
+  constexpr bool rowmap = Extra::MAPPED;  // rows of A are gathered
   const char* a0 = (const char*)A.p + (C::TA ? (size_t)m0 : rowmap ? 0 : (size_t)m0 * A.ld) * C::ES;
   const char* b0 = (const char*)B.p + (C::TB ? (size_t)n0 : PAIR ? 0 : (size_t)n0 * B.ld) * C::ES;
   auto arow = [&](int r) {
@@ -358,7 +357,7 @@ __device__ __forceinline__ void product(const Operand A, const Operand B, int K,
   // wait for the next k-tile.  A k-tile's copies lie between the products of
   // the k-tile SLOTS - 1 before it.
   const int KF = K / C::BK;
-  static_assert(C::NSUB % 2 == 0 && NP % 4 == 0, "substeps in pairs");
+  static_assert(C::NSUB % 2 == 0, "substeps in pairs");
   Frags f[2];
   if (KF > 0) {
     landed();
@@ -445,7 +444,7 @@ __global__ __launch_bounds__(C::NTHR, 1) void product_kernel(Operand A, Operand 
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS_BYTES];
   int tm, tn;
   if (!tile_of(blockIdx.x, mt, nt, tm, tn)) return;
-  product<C, Epi, Extra>(A, B, K, half, tm, tn, epi, extra, smem);
+  product<C, Epi, Extra>(A, B, K, half, tm * C::BM, tn * (Epi::PAIR ? C::BN / 2 : C::BN), epi, extra, smem);
 }
 
 template <class C, class Epi, class Extra = NoExtra>

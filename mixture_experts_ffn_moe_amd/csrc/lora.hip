@@ -246,7 +246,7 @@ __global__ __launch_bounds__(C::NTHR) void shrink_kernel(const typename C::E* x,
 template <class E>
 struct AddLora {
   static constexpr bool ON = true, MAPPED = true;
-  const int32_t *perm, *sorted;
+  const int32_t *perm, *sorted, *first;
   const float* v;  // [parts, T, r]
   const E* b;      // [L, rows, r]
   int T, L, r, rows, parts;
@@ -254,79 +254,127 @@ struct AddLora {
   __device__ __forceinline__ int a_row(int p) const { return perm[p]; }
   __device__ __forceinline__ int out_row(int p) const { return perm[p]; }
 
-  // 16 bytes of low-rank values of position p from rank k (zeros past r),
-  // rounded to the layer's type as the matrix operand they are.
-  __device__ __forceinline__ typename Mma<E, 16>::frag values(int p, int k) const {
-    constexpr int N = 16 / sizeof(E);
-    typename Mma<E, 16>::frag f;
-    float t[N] = {};
-    if (k < r) {
-      for (int s = 0; s < parts; ++s) {
-        const float* q = v + ((size_t)s * T + p) * r + k;
+  // The runs of equal adapters among a tile's rows: run n is tile rows
+  // start .. next start, start << 16 | adapter.
+  template <int BM>
+  struct Runs {
+    uint32_t run[BM + 1];
+    int count;
+  };
+  template <int BM>
+  static __device__ __forceinline__ Runs<BM>& runs() {
+    __shared__ Runs<BM> s;
+    return s;
+  }
+  template <class C>
+  __device__ __forceinline__ void begin(int m0, int wave, int lane) const {
+    if (wave != 0) return;
+    Runs<C::BM>& s = runs<C::BM>();
+    int n = 0;
 #pragma unroll
-        for (int e = 0; e < N; e += 4) {
-          const f32x4 o = *reinterpret_cast<const f32x4*>(q + e);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) t[e + i] += o[i];
-        }
-      }
+    for (int r0 = 0; r0 < C::BM; r0 += 64) {
+      const int row = r0 + lane, p = m0 + row;
+      const int mine = row < C::BM && p < T ? sorted[p] : L;
+      const int left = row > 0 && row < C::BM && p < T ? sorted[p - 1] : -1;
+      const bool start = mine != left && mine < L;
+      const uint64_t mask = __ballot(start);
+      if (start) s.run[n + __popcll(mask & ((1ull << lane) - 1))] = (uint32_t)row << 16 | (uint32_t)mine;
+      n += __popcll(mask);
     }
-#pragma unroll
-    for (int e = 0; e < N; ++e) {
-      if constexpr (sizeof(E) == 2) f[e] = (__bf16)t[e];
-      else f[e] = t[e];
+    // the end of the last run: tokens without an adapter come last
+    const int end = min(first[L] - m0, C::BM);
+    if (lane == 0) {
+      s.run[n] = (uint32_t)(n ? end : 0) << 16;
+      s.count = n;
     }
-    return f;
   }
 
-  // m: the wave's first position; brow(j): this lane's row of b in fragment j.
-  template <class C, class Row>
-  __device__ __forceinline__ void add(typename C::M::acc (&acc)[C::FM][C::FN], int m, Row brow, int lane) const {
-    constexpr int KS = 4;  // matrix steps whose low-rank values a lane holds at a time
-    const int kl = (lane / C::F) * C::EPC;
-    const E* pb[C::FN];
+  // Adds B_a v to the tile's accumulators, the ring's LDS in use for it: the
+  // tile's low-rank values of RS ranks (summed over the parts and rounded to
+  // the layer's type as the matrix operand they are), and a ring of the B rows
+  // of the tile's adapters, copied ahead.  b_r0(j): first tile row of this
+  // wave's fragment j; brow(i): row of B of tile row i.
+  template <class C, class R0, class Row>
+  __device__ __forceinline__ void add(typename C::M::acc (&acc)[C::FM][C::FN], char* smem, int m0, int wave_m, R0 b_r0,
+                                      Row brow, int wave, int lane) const {
+    typedef Cfg<E, C::BM, C::BN, C::WM, C::WN, C::F, 128, 2, false, false> S;  // tiles of 128-byte rows
+    constexpr int RS = 128 / sizeof(E);
+    constexpr int RING = (C::LDS_BYTES - S::A_BYTES) / S::B_BYTES < 6 ? (C::LDS_BYTES - S::A_BYTES) / S::B_BYTES : 6;
+    static_assert(RING >= 2 && (RING - 2) * S::BQ < 64, "ring of B tiles");
+    const Runs<C::BM>& list = runs<C::BM>();
+    const int count = __builtin_amdgcn_readfirstlane(list.count);
+    if (count == 0) return;
+    const uint32_t lds = (uint32_t)(uintptr_t)smem + S::A_BYTES;
+    for (int k0 = 0; k0 < r; k0 += RS) {
+      const int left = min(RS, r - k0);
+      if (k0) __syncthreads();
+      uint32_t off[S::BQ];
+      tile::copy_offsets<S, false, C::BN>(off, 0, 0, r, left, wave, lane, brow);
+      int sent = 0;
+      auto copy = [&]() {  // past the last run, its B again: every wait counts the same
+        const uint32_t a = __builtin_amdgcn_readfirstlane(list.run[min(sent, count - 1)]) & 0xffffu;
+        const char* p = uniform_ptr((const char*)(b + (size_t)a * rows * r + k0));
 #pragma unroll
-    for (int j = 0; j < C::FN; ++j) pb[j] = b + (size_t)brow(j) * r + kl;
+        for (int i = 0; i < S::BQ; ++i)
+          dma16(lds + (uint32_t)((sent % RING) * S::B_BYTES) + (uint32_t)(wave + C::NW * i) * 1024u, p, off[i]);
+        ++sent;
+      };
+      for (int n = 0; n < RING - 1; ++n) copy();
+      // low-rank values, 16 bytes at a time, zeros past the rank
+      constexpr int N = 16 / sizeof(E);
+      for (int e = wave * 64 + lane; e < C::BM * 8; e += C::NTHR) {
+        const int row = e >> 3, c = e & 7;
+        f32x4 t[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        if (m0 + row < T && c * N < left)
+          for (int s = 0; s < parts; ++s) {
+            const float* q = v + ((size_t)s * T + m0 + row) * r + k0 + c * N;
 #pragma unroll
-    for (int i = 0; i < C::FM; ++i) {
-      const int p = min(m + C::F * i + lane % C::F, T - 1);
-      const int mine = sorted[p];
-      const int lead = __builtin_amdgcn_readfirstlane(mine);
-      if (lead >= L) continue;
-      for (int k0 = 0; k0 < r; k0 += KS * C::M::SUB) {
-        typename C::M::frag fv[KS];
+            for (int h = 0; h < N / 4; ++h) t[h] += reinterpret_cast<const f32x4*>(q)[h];
+          }
+        char* to = smem + row * 128 + (c ^ tile::swz_row<128>(row)) * 16;
+        if constexpr (sizeof(E) == 2) {
+          const uint2 lo = pack_bf16x4(t[0]), hi = pack_bf16x4(t[1]);
+          *reinterpret_cast<uint4*>(to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+        } else {
+          *reinterpret_cast<f32x4*>(to) = t[0];
+        }
+      }
+      for (int n = 0; n < count; ++n) {
+        wait_vmcnt<(RING - 2) * S::BQ>();  // this run's B
+        tile::slot_barrier();
+        const int r0 = __builtin_amdgcn_readfirstlane(list.run[n]) >> 16, r1 = __builtin_amdgcn_readfirstlane(list.run[n + 1]) >> 16;
+        copy();
+        const char* tb = smem + S::A_BYTES + (n % RING) * S::B_BYTES;
 #pragma unroll
-        for (int k = 0; k < KS; ++k) fv[k] = values(p, k0 + k * C::M::SUB + kl);
-        int cur = lead;
-        while (cur < L) {
+        for (int i = 0; i < C::FM; ++i) {
+          const int f0 = wave_m + C::F * i;
+          if (f0 >= r1 || f0 + C::F <= r0) continue;
           typename C::M::acc d[C::FN];
 #pragma unroll
           for (int j = 0; j < C::FN; ++j)
 #pragma unroll
             for (int e = 0; e < C::F * C::F / 64; ++e) d[j][e] = 0.0f;
-          const size_t at = (size_t)cur * rows * r + k0;
-#pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            if (k0 + k * C::M::SUB >= r) break;
+          for (int ks = 0; ks * C::M::SUB < left; ++ks) {
+            const int some = left - ks * C::M::SUB;
+            const typename C::M::frag fv = tile::read_frag<S, false, C::BM>(smem, wave_m + C::F * i, ks, lane);
 #pragma unroll
             for (int j = 0; j < C::FN; ++j) {
-              typename C::M::frag fb = {};
-              if (k0 + k * C::M::SUB + kl < r)
-                fb = *reinterpret_cast<const typename C::M::frag*>(pb[j] + at + k * C::M::SUB);
-              d[j] = C::M::mul(fb, fv[k], d[j]);
+              typename C::M::frag fb = tile::read_frag<S, false, C::BN>(tb, b_r0(j), ks, lane);
+              if (some < C::M::SUB) fb = tile::mask_k<S>(fb, some, lane);
+              d[j] = C::M::mul(fb, fv, d[j]);
             }
           }
           tile::settle();
           // every lane holds one row: it takes the product of its own adapter
+          const int row = f0 + lane % C::F;
+          const bool mine = row >= r0 && row < r1;
 #pragma unroll
           for (int j = 0; j < C::FN; ++j)
 #pragma unroll
-            for (int e = 0; e < C::F * C::F / 64; ++e) acc[i][j][e] = mine == cur ? acc[i][j][e] + d[j][e] : acc[i][j][e];
-          const uint64_t later = __ballot(mine > cur);
-          if (later == 0) break;
-          cur = __builtin_amdgcn_readlane(mine, __ffsll((long long)later) - 1);
+            for (int e = 0; e < C::F * C::F / 64; ++e) acc[i][j][e] = mine ? acc[i][j][e] + d[j][e] : acc[i][j][e];
         }
       }
+      wait_vmcnt<0>();
     }
   }
 };
@@ -362,17 +410,10 @@ hipError_t big(const Ffn& f, const Lora& l, const void* x, int K, const void* w,
   const hipError_t e = l.r <= 32 ? shrink(Cfg<E, 32, 32, 1, 2, 16, 128, 4, false, false>{})
                                  : shrink(Cfg<E, 32, 64, 1, 4, 16, 128, 4, false, false>{});
   if (e != hipSuccess) return e;
-  const AddLora<E> add{s.perm, s.sorted, s.v, (const E*)b, f.T, l.L, l.r, rows, parts};
+  const AddLora<E> add{s.perm, s.sorted, s.first, s.v, (const E*)b, f.T, l.L, l.r, rows, parts};
   const Operand A{x, K, f.T}, B{w, K, rows};
   const int half = Epi::PAIR ? rows / 2 : 0;
-  auto tiles = [&](int bm, int bn) { return (long long)((f.T + bm - 1) / bm) * ((rows + bn - 1) / bn); };
-  if constexpr (sizeof(E) == 2) {
-    if (tiles(256, 256) >= 192) return tile::launch_product<Cfg<E, 256, 256, 2, 4, 32, 64, 4, false, false>>(A, B, K, half, epi, st, add);
-    if (tiles(128, 128) >= 192) return tile::launch_product<Cfg<E, 128, 128, 2, 2, 32, 128, 4, false, false>>(A, B, K, half, epi, st, add);
-  } else {
-    if (tiles(128, 128) >= 192) return tile::launch_product<Cfg<E, 128, 128, 2, 2, 16, 128, 4, false, false>>(A, B, K, half, epi, st, add);
-  }
-  return tile::launch_product<Cfg<E, 64, 64, 2, 2, 16, 128, 4, false, false>>(A, B, K, half, epi, st, add);
+  return tile::run_product<E, false, false>(A, B, K, half, epi, st, add);
 }
 
 // ---------------------------------------------------------------------------

@@ -101,15 +101,17 @@ __device__ __forceinline__ int swz_row(int row) {
   return KB == 128 ? (row >> 1) & 7 : (row >> 2) & 3;
 }
 
-// Swizzle of a k-rows tile of C columns: XOR of the 16-column unit of row k.
-// 32 lanes of a bf16 read take four rows (F = 32: of two adjacent units) or
-// eight (F = 16: k and k + 8, of one unit); the XOR sends them to the eight
-// 32-byte slots of 256 bytes.  fp32 reads take four rows, four apart.
+// Swizzle of a k-rows tile of C columns: XOR of the 16-column unit of row k,
+// below the number of units of a row.  32 lanes of a bf16 read take four rows
+// (F = 32: of two adjacent units) or eight (F = 16: k and k + 8, of one unit);
+// the XOR sends them to the eight 32-byte slots of 256 bytes.  fp32 reads take
+// four rows, four apart (two of them meet where a row has two units only).
 template <class E, int F, int C>
 __device__ __forceinline__ int swz_k(int k) {
-  if (sizeof(E) == 4) return (k >> 2) & 3;
+  static_assert(C >= 128 || C == 64 || (C == 32 && F == 16), "units of a row");
+  if (sizeof(E) == 4) return (k >> 2) & (C >= 64 ? 3 : 1);
   if (F == 32) return C >= 128 ? (k & 3) << 1 : k & 2;
-  return C >= 128 ? (k & 3) | ((k >> 1) & 4) : ((k >> 1) & 1) | ((k >> 2) & 2);
+  return C >= 128 ? (k & 3) | ((k >> 1) & 4) : C == 64 ? ((k >> 1) & 1) | ((k >> 2) & 2) : (k >> 3) & 1;
 }
 
 // Source byte offsets of a wave's direct copies of one operand tile, relative
@@ -201,24 +203,15 @@ __device__ __forceinline__ void settle() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Tile of this workgroup.  Block b runs on die b % 8; each die takes a
-// contiguous range of tiles, which run down groups of 8 row tiles, so that
-// the 32 tiles a die works on at a time share their rows and columns in its L2.
-__device__ __forceinline__ bool tile_of(int b, int mt, int nt, int& m, int& n) {
-  const int all = mt * nt, per = (all + kXcds - 1) / kXcds;
-  const int slot = b / kXcds, t = (b % kXcds) * per + slot;
-  if (slot >= per || t >= all) return false;
+// Tile t of mt x nt: tiles run down groups of 8 row tiles, so that the 32
+// tiles a die works on at a time share their rows and columns in its L2.
+__device__ __forceinline__ void tile_of(int t, int mt, int nt, int& m, int& n) {
   constexpr int G = 8;
   const int group = t / (G * nt), in = t - group * (G * nt);
   const int rows = min(G, mt - group * G);
   m = group * G + in % rows;
   n = in / rows;
-  return true;
 }
-
-struct Identity {
-  __device__ __forceinline__ int operator()(int r) const { return r; }
-};
 
 // No low-rank addition.
 struct NoExtra {
@@ -306,6 +299,7 @@ __device__ __forceinline__ void product(const Operand A, const Operand B, int K,
       for (int i = 0; i < NI; ++i) copy_piece(i);
     }
   }
+  if constexpr (Extra::ON) extra.template begin<C>(m0, wave, lane);
   // The next k-tile has landed for every wave, and the slot of the one before it is free.
   auto landed = [&]() {
     wait_vmcnt<(C::SLOTS - 2) * NI>();
@@ -389,16 +383,17 @@ __device__ __forceinline__ void product(const Operand A, const Operand B, int K,
       multiply(t, 0, NP, nullptr, nullptr, 0, 0, 0);
     }
   }
-  if constexpr (Extra::ON) extra.template add<C>(acc, m0 + wm * C::TM, [&](int j) {
-    const int r = b_r0(j) + lane % C::F;
-    if (!PAIR) return min(n0 + r, N - 1);
-    const int up = r >= C::BN / 2;
-    return up * half + min(n0 + r - up * (C::BN / 2), half - 1);
-  }, lane);
-
   settle();
   wait_vmcnt<0>();  // copies that nothing waited for
   __syncthreads();  // every wave is past its last LDS read: the ring is free
+  if constexpr (Extra::ON) {
+    extra.template add<C>(acc, smem, m0, wm * C::TM, b_r0, [&](int r) {
+      const int up = PAIR && r >= C::BN / 2;
+      return up * half + min(n0 + r - up * (C::BN / 2), N - 1);
+    }, wave, lane);
+    settle();
+    __syncthreads();
+  }
   float* strip = reinterpret_cast<float*>(smem + wave * C::STRIP_BYTES);
   constexpr int WC = PAIR ? C::TN / 2 : C::TN;  // output columns of the wave
   constexpr int LPR = WC / 8, RPI = 64 / LPR;   // lanes of a row, rows of an iteration
@@ -438,24 +433,110 @@ __device__ __forceinline__ void product(const Operand A, const Operand B, int K,
   }
 }
 
+// Block b runs on die b % 8; each die takes a contiguous range of tiles.
 template <class C, class Epi, class Extra>
 __global__ __launch_bounds__(C::NTHR, 1) void product_kernel(Operand A, Operand B, int K, int half, int mt, int nt,
                                                              Epi epi, Extra extra) {
   __shared__ __attribute__((aligned(1024))) char smem[C::LDS_BYTES];
+  const int all = mt * nt, per = (all + kXcds - 1) / kXcds;
+  const int slot = blockIdx.x / kXcds, t = (blockIdx.x % kXcds) * per + slot;
+  if (slot >= per || t >= all) return;
   int tm, tn;
-  if (!tile_of(blockIdx.x, mt, nt, tm, tn)) return;
+  tile_of(t, mt, nt, tm, tn);
   product<C, Epi, Extra>(A, B, K, half, tm * C::BM, tn * (Epi::PAIR ? C::BN / 2 : C::BN), epi, extra, smem);
 }
 
-template <class C, class Epi, class Extra = NoExtra>
-hipError_t launch_product(Operand A, Operand B, int K, int half, const Epi& epi, hipStream_t st,
-                          const Extra& extra = Extra{}) {
+template <class C, class Epi, class Extra>
+hipError_t launch_product(Operand A, Operand B, int K, int half, const Epi& epi, hipStream_t st, const Extra& extra) {
   const int oc = Epi::PAIR ? C::BN / 2 : C::BN, N = Epi::PAIR ? half : B.count;
   const int mt = (A.count + C::BM - 1) / C::BM, nt = (N + oc - 1) / oc;
   const unsigned grid = (unsigned)(((long long)mt * nt + kXcds - 1) / kXcds * kXcds);
   hipLaunchKernelGGL((product_kernel<C, Epi, Extra>), dim3(grid), dim3(C::NTHR), 0, st, A, B, K, half, mt, nt, epi,
                      extra);
   return hipGetLastError();
+}
+
+// The tile sizes a product may take, and what one costs: ns per 128 bytes of k
+// with 1, 2, ... workgroups on every CU (as many as LDS holds), measured at
+// K = 4096 (bf16, average of a product with both operands k-contiguous and
+// one with both k-rows) and 2048 (fp32), and ns a tile beside that.
+struct TileCost {
+  int bm, bn, resident;
+  int step[3];
+};
+template <class E>
+struct TileCosts;
+template <>
+struct TileCosts<uint16_t> {
+  static constexpr int COUNT = 6;
+  static constexpr TileCost C[COUNT] = {{32, 64, 3, {185, 310, 460}}, {64, 64, 2, {210, 370, 0}}, {64, 128, 1, {305, 0, 0}},
+                                        {128, 128, 1, {490, 0, 0}},   {128, 256, 1, {900, 0, 0}}, {256, 256, 1, {1630, 0, 0}}};
+};
+template <>
+struct TileCosts<float> {
+  static constexpr int COUNT = 4;
+  static constexpr TileCost C[COUNT] = {{32, 64, 3, {300, 540, 770}}, {64, 64, 2, {520, 980, 0}}, {64, 128, 1, {1000, 0, 0}},
+                                        {128, 128, 1, {1890, 0, 0}}};
+};
+template <class E, int I, bool TA, bool TB>
+struct TileCfg;
+template <bool TA, bool TB> struct TileCfg<uint16_t, 0, TA, TB> { typedef Cfg<uint16_t, 32, 64, 2, 2, 16, 128, 4, TA, TB> type; };
+template <bool TA, bool TB> struct TileCfg<uint16_t, 1, TA, TB> { typedef Cfg<uint16_t, 64, 64, 2, 2, 16, 128, 4, TA, TB> type; };
+template <bool TA, bool TB> struct TileCfg<uint16_t, 2, TA, TB> { typedef Cfg<uint16_t, 64, 128, 2, 4, 16, 128, 4, TA, TB> type; };
+template <bool TA, bool TB> struct TileCfg<uint16_t, 3, TA, TB> { typedef Cfg<uint16_t, 128, 128, 2, 2, 32, 128, 4, TA, TB> type; };
+template <bool TA, bool TB> struct TileCfg<uint16_t, 4, TA, TB> { typedef Cfg<uint16_t, 128, 256, 2, 4, 32, 128, 3, TA, TB> type; };
+template <bool TA, bool TB> struct TileCfg<uint16_t, 5, TA, TB> { typedef Cfg<uint16_t, 256, 256, 2, 4, 32, 64, 4, TA, TB> type; };
+template <bool TA, bool TB> struct TileCfg<float, 0, TA, TB> { typedef Cfg<float, 32, 64, 2, 2, 16, 128, 4, TA, TB> type; };
+template <bool TA, bool TB> struct TileCfg<float, 1, TA, TB> { typedef Cfg<float, 64, 64, 4, 2, 16, 128, 4, TA, TB> type; };
+template <bool TA, bool TB> struct TileCfg<float, 2, TA, TB> { typedef Cfg<float, 64, 128, 2, 4, 16, 128, 4, TA, TB> type; };
+template <bool TA, bool TB> struct TileCfg<float, 3, TA, TB> { typedef Cfg<float, 128, 128, 2, 4, 16, 128, 4, TA, TB> type; };
+
+inline long long tile_ns(const TileCost& c, long long steps, int resident) {
+  return steps * c.step[resident - 1] + 1500 + c.bm * c.bn / 10;
+}
+constexpr int kCus = 256;
+// Estimated ns of an M x N product: whole rounds of `resident` tiles a CU, and
+// what is left.
+inline long long product_ns(const TileCost& c, long long M, long long N, long long steps) {
+  const long long tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn), a_cu = (tiles + kCus - 1) / kCus;
+  const int left = (int)(a_cu % c.resident);
+  return a_cu / c.resident * tile_ns(c, steps, c.resident) + (left ? tile_ns(c, steps, left) : 0);
+}
+template <class E, class F>
+int cheapest(F ns) {
+  int best = 0;
+  for (int i = 1; i < TileCosts<E>::COUNT; ++i)
+    if (ns(TileCosts<E>::C[i]) < ns(TileCosts<E>::C[best])) best = i;
+  return best;
+}
+// f(index constant) for tile size i.
+template <int I>
+struct Index {
+  static constexpr int value = I;
+};
+template <class E, class F>
+hipError_t with_tile(int i, F f) {
+  switch (i) {
+    case 0: return f(Index<0>{});
+    case 1: return f(Index<1>{});
+    case 2: return f(Index<2>{});
+    default: break;
+  }
+  if constexpr (TileCosts<E>::COUNT > 4) {
+    if (i == 4) return f(Index<4>{});
+    if (i == 5) return f(Index<5>{});
+  }
+  return f(Index<3>{});
+}
+// The product with the tile size that is estimated to be the fastest.
+template <class E, bool TA, bool TB, class Epi, class Extra = NoExtra>
+hipError_t run_product(const Operand& A, const Operand& B, int K, int half, const Epi& epi, hipStream_t st,
+                       const Extra& extra = Extra{}) {
+  const long long N = Epi::PAIR ? 2ll * half : B.count, steps = ((long long)K * sizeof(E) + 127) / 128;
+  const int i = cheapest<E>([&](const TileCost& c) { return product_ns(c, A.count, N, steps); });
+  return with_tile<E>(i, [&](auto index) {
+    return launch_product<typename TileCfg<E, decltype(index)::value, TA, TB>::type>(A, B, K, half, epi, st, extra);
+  });
 }
 
 // ---------------------------------------------------------------------------

@@ -124,10 +124,10 @@ moe_status moe_shared_ffn_backward(const moe_shape* shape, int32_t Is, double p,
     MOE_CHECK(check_ptr(w2s)); MOE_CHECK(check_ptr(gu)); MOE_CHECK(check_ptr(d_out));
     MOE_CHECK(check_workspace(workspace, workspace_bytes, backward_bytes(f)));
     MOE_CHECK(hip_status(moe::launch_train_dgu(f, d, d_out, w2s, gu, workspace, st)));
-    if (d_x) MOE_CHECK(hip_status(moe::launch_train_dx(f, workspace, w1s, d_x, st)));
+  } else if (d_w1s == nullptr) {
+    return MOE_OK;
   }
-  if (d_w1s) return hip_status(moe::launch_train_dw(f, x, hs, d_out, workspace, d_w1s, d_w2s, st));
-  return MOE_OK;
+  return hip_status(moe::launch_train_gradients(f, x, w1s, hs, d_out, workspace, d_x, d_w1s, d_w2s, st));
 }
 
 size_t moe_lora_workspace_size(const moe_shape* shape, int32_t Is, const moe_lora_spec* spec) {

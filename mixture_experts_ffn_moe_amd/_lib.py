@@ -537,38 +537,69 @@ def moe_finalize_backward(shape, y, inv, d_out, d_topk_w, stream=None):
 
 # ---- shared expert's training and dropout (moe_shared_train.h)
 
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
 
-def _rng_arg(p, rng):
+
+def _here() -> int:
+    """The current device (without torch.cuda's initialisation check: a GPU tensor exists, or no argument passes)."""
+    try:
+        return _get_device() if _get_device is not None else torch.cuda.current_device()
+    except RuntimeError:
+        return -2
+
+
+def _on(here: int, name: str, t, dtype: torch.dtype, numel: int, nullable: bool = False):
+    """_arg for a tensor that has to be on the current device."""
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.numel() == numel and t.get_device() == here and t.is_contiguous():
+        return t.data_ptr()
+    p = _arg(name, t, dtype, numel, nullable)
+    if t is not None:
+        _on_current(t)
+    return p
+
+
+def _workspace_on(here: int, workspace):
+    ws, nbytes = _workspace(workspace)
+    if workspace.get_device() != here:
+        _on_current(workspace)
+    return ws, nbytes
+
+
+def _stream_on(here: int, stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(here)
+    _on_current(stream=stream)
+    return _stream(stream)
+
+
+def _rng_on(here: int, p, rng):
     """The random stream's seed and offset (an int64 tensor of two on the GPU); unread where nothing is dropped."""
-    return _arg("rng", rng, torch.int64, 2, nullable=not p >= 1 / 131072)
+    return _on(here, "rng", rng, torch.int64, 2, nullable=not p >= 1 / 131072)
 
 
 def moe_dropout_add(shape, p, rng, y, residual, out, stream=None):
     """out = residual (or None) + dropout(y); rng: int64 [2] on the GPU, seed and offset."""
-    n, dt = shape.T * shape.H, _layer_dtype(shape)
-    args = (_rng_arg(p, rng), _arg("y", y, dt, n), _arg("residual", residual, dt, n, nullable=True),
-            _arg("out", out, dt, n))
-    _on_current(rng, y, residual, out, stream=stream)
-    _check(lib.moe_dropout_add(ctypes.byref(shape), float(p), *args, _stream(stream)), "moe_dropout_add")
+    n, dt, here = shape.T * shape.H, _layer_dtype(shape), _here()
+    _check(lib.moe_dropout_add(ctypes.byref(shape), p, _rng_on(here, p, rng), _on(here, "y", y, dt, n),
+                               _on(here, "residual", residual, dt, n, True), _on(here, "out", out, dt, n),
+                               _stream_on(here, stream)), "moe_dropout_add")
 
 
 def moe_dropout_backward(shape, p, rng, d_out, d_y, stream=None):
     """Gradient of moe_dropout_add's y, with the forward call's p and rng."""
-    n, dt = shape.T * shape.H, _layer_dtype(shape)
-    args = (_rng_arg(p, rng), _arg("d_out", d_out, dt, n), _arg("d_y", d_y, dt, n))
-    _on_current(rng, d_out, d_y, stream=stream)
-    _check(lib.moe_dropout_backward(ctypes.byref(shape), float(p), *args, _stream(stream)), "moe_dropout_backward")
+    n, dt, here = shape.T * shape.H, _layer_dtype(shape), _here()
+    _check(lib.moe_dropout_backward(ctypes.byref(shape), p, _rng_on(here, p, rng), _on(here, "d_out", d_out, dt, n),
+                                    _on(here, "d_y", d_y, dt, n), _stream_on(here, stream)), "moe_dropout_backward")
 
 
 def moe_shared_ffn_train(shape, Is, p, rng, x, w1s, w2s, residual, gu, hs, out, stream=None):
     """The shared expert's forward pass with dropout of its hidden values; keeps gu (fp32) and hs for the backward pass."""
-    T, H, dt = shape.T, shape.H, _layer_dtype(shape)
-    args = (_rng_arg(p, rng), _arg("x", x, dt, T * H), _arg("w1s", w1s, dt, 2 * Is * H), _arg("w2s", w2s, dt, H * Is),
-            _arg("residual", residual, dt, T * H, nullable=True), _arg("gu", gu, torch.float32, T * 2 * Is),
-            _arg("hs", hs, dt, T * Is), _arg("out", out, dt, T * H))
-    _on_current(rng, x, w1s, w2s, residual, gu, hs, out, stream=stream)
-    _check(lib.moe_shared_ffn_train(ctypes.byref(shape), int(Is), float(p), *args, _stream(stream)),
-           "moe_shared_ffn_train")
+    T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
+    _check(lib.moe_shared_ffn_train(ctypes.byref(shape), Is, p, _rng_on(here, p, rng), _on(here, "x", x, dt, T * H),
+                                    _on(here, "w1s", w1s, dt, 2 * Is * H), _on(here, "w2s", w2s, dt, H * Is),
+                                    _on(here, "residual", residual, dt, T * H, True),
+                                    _on(here, "gu", gu, torch.float32, T * 2 * Is), _on(here, "hs", hs, dt, T * Is),
+                                    _on(here, "out", out, dt, T * H), _stream_on(here, stream)), "moe_shared_ffn_train")
 
 
 def moe_shared_backward_workspace_size(shape: MoeShape, Is: int) -> int:
@@ -577,16 +608,15 @@ def moe_shared_backward_workspace_size(shape: MoeShape, Is: int) -> int:
 
 def moe_shared_ffn_backward(shape, Is, p, rng, x, w1s, w2s, gu, hs, d_out, d_x, d_w1s, d_w2s, workspace, stream=None):
     """Gradients of x (unless d_x is None) and of both weights (unless d_w1s and d_w2s are None)."""
-    T, H, dt = shape.T, shape.H, _layer_dtype(shape)
+    T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
     no_x, no_w = d_x is None, d_w1s is None and d_w2s is None
-    args = (_rng_arg(p, rng), _arg("x", x, dt, T * H, nullable=no_w), _arg("w1s", w1s, dt, 2 * Is * H, nullable=no_x),
-            _arg("w2s", w2s, dt, H * Is), _arg("gu", gu, torch.float32, T * 2 * Is), _arg("hs", hs, dt, T * Is, nullable=no_w),
-            _arg("d_out", d_out, dt, T * H), _arg("d_x", d_x, dt, T * H, nullable=True),
-            _arg("d_w1s", d_w1s, dt, 2 * Is * H, nullable=True), _arg("d_w2s", d_w2s, dt, H * Is, nullable=True))
-    ws, nbytes = _workspace(workspace)
-    _on_current(rng, x, w1s, w2s, gu, hs, d_out, d_x, d_w1s, d_w2s, workspace, stream=stream)
-    _check(lib.moe_shared_ffn_backward(ctypes.byref(shape), int(Is), float(p), *args, ws, nbytes, _stream(stream)),
-           "moe_shared_ffn_backward")
+    _check(lib.moe_shared_ffn_backward(
+        ctypes.byref(shape), Is, p, _rng_on(here, p, rng), _on(here, "x", x, dt, T * H, no_w),
+        _on(here, "w1s", w1s, dt, 2 * Is * H, no_x), _on(here, "w2s", w2s, dt, H * Is),
+        _on(here, "gu", gu, torch.float32, T * 2 * Is), _on(here, "hs", hs, dt, T * Is, no_w),
+        _on(here, "d_out", d_out, dt, T * H), _on(here, "d_x", d_x, dt, T * H, True),
+        _on(here, "d_w1s", d_w1s, dt, 2 * Is * H, True), _on(here, "d_w2s", d_w2s, dt, H * Is, True), *_workspace_on(here, workspace),
+        _stream_on(here, stream)), "moe_shared_ffn_backward")
 
 
 # ---- request adapters (moe_lora.h)
@@ -601,52 +631,40 @@ def moe_lora_workspace_size(shape: MoeShape, Is: int, lora: MoeLoraSpec) -> int:
     return int(lib.moe_lora_workspace_size(ctypes.byref(shape), int(Is), ctypes.byref(lora)))
 
 
-def _w13_adapters(lora, Is, H, dt, a1, b1):
-    n = lora.adapters * lora.rank
-    return _arg("a1", a1, dt, n * H), _arg("b1", b1, dt, n * 2 * Is)
-
-
-def _down_adapters(lora, Is, H, dt, a2, b2):
-    n = lora.adapters * lora.rank
-    return _arg("a2", a2, dt, n * Is), _arg("b2", b2, dt, n * H)
-
-
 def moe_lora_w13_swiglu(shape, Is, lora, x, w1s, a1, b1, scale, adapter_ids, hs, workspace, stream=None):
     """SwiGLU of the shared expert's gate and up projection, every token with its own adapter."""
-    T, H, dt = shape.T, shape.H, _layer_dtype(shape)
-    args = (_arg("x", x, dt, T * H), _arg("w1s", w1s, dt, 2 * Is * H), *_w13_adapters(lora, Is, H, dt, a1, b1),
-            _arg("scale", scale, torch.float32, lora.adapters), _arg("adapter_ids", adapter_ids, torch.int32, T),
-            _arg("hs", hs, dt, T * Is))
-    ws, nbytes = _workspace(workspace)
-    _on_current(x, w1s, a1, b1, scale, adapter_ids, hs, workspace, stream=stream)
-    _check(lib.moe_lora_w13_swiglu(ctypes.byref(shape), int(Is), ctypes.byref(lora), *args, ws, nbytes,
-                                   _stream(stream)), "moe_lora_w13_swiglu")
+    T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
+    L, n = lora.adapters, lora.adapters * lora.rank
+    _check(lib.moe_lora_w13_swiglu(
+        ctypes.byref(shape), Is, ctypes.byref(lora), _on(here, "x", x, dt, T * H), _on(here, "w1s", w1s, dt, 2 * Is * H),
+        _on(here, "a1", a1, dt, n * H), _on(here, "b1", b1, dt, n * 2 * Is), _on(here, "scale", scale, torch.float32, L),
+        _on(here, "adapter_ids", adapter_ids, torch.int32, T), _on(here, "hs", hs, dt, T * Is), *_workspace_on(here, workspace),
+        _stream_on(here, stream)), "moe_lora_w13_swiglu")
 
 
 def moe_lora_down(shape, Is, lora, hs, w2s, a2, b2, scale, adapter_ids, residual, out, workspace, stream=None):
     """The shared expert's down projection, every token with its own adapter, plus the residual (or None)."""
-    T, H, dt = shape.T, shape.H, _layer_dtype(shape)
-    args = (_arg("hs", hs, dt, T * Is), _arg("w2s", w2s, dt, H * Is), *_down_adapters(lora, Is, H, dt, a2, b2),
-            _arg("scale", scale, torch.float32, lora.adapters), _arg("adapter_ids", adapter_ids, torch.int32, T),
-            _arg("residual", residual, dt, T * H, nullable=True), _arg("out", out, dt, T * H))
-    ws, nbytes = _workspace(workspace)
-    _on_current(hs, w2s, a2, b2, scale, adapter_ids, residual, out, workspace, stream=stream)
-    _check(lib.moe_lora_down(ctypes.byref(shape), int(Is), ctypes.byref(lora), *args, ws, nbytes, _stream(stream)),
-           "moe_lora_down")
+    T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
+    L, n = lora.adapters, lora.adapters * lora.rank
+    _check(lib.moe_lora_down(
+        ctypes.byref(shape), Is, ctypes.byref(lora), _on(here, "hs", hs, dt, T * Is), _on(here, "w2s", w2s, dt, H * Is),
+        _on(here, "a2", a2, dt, n * Is), _on(here, "b2", b2, dt, n * H), _on(here, "scale", scale, torch.float32, L),
+        _on(here, "adapter_ids", adapter_ids, torch.int32, T), _on(here, "residual", residual, dt, T * H, True),
+        _on(here, "out", out, dt, T * H), *_workspace_on(here, workspace), _stream_on(here, stream)), "moe_lora_down")
 
 
 def moe_shared_ffn_lora(shape, Is, lora, x, w1s, w2s, a1, b1, a2, b2, scale, adapter_ids, residual, hs, out, workspace,
                         stream=None):
     """The shared expert with adapters on both projections, plus the residual (or None)."""
-    T, H, dt = shape.T, shape.H, _layer_dtype(shape)
-    args = (_arg("x", x, dt, T * H), _arg("w1s", w1s, dt, 2 * Is * H), _arg("w2s", w2s, dt, H * Is),
-            *_w13_adapters(lora, Is, H, dt, a1, b1), *_down_adapters(lora, Is, H, dt, a2, b2),
-            _arg("scale", scale, torch.float32, lora.adapters), _arg("adapter_ids", adapter_ids, torch.int32, T),
-            _arg("residual", residual, dt, T * H, nullable=True), _arg("hs", hs, dt, T * Is), _arg("out", out, dt, T * H))
-    ws, nbytes = _workspace(workspace)
-    _on_current(x, w1s, w2s, a1, b1, a2, b2, scale, adapter_ids, residual, hs, out, workspace, stream=stream)
-    _check(lib.moe_shared_ffn_lora(ctypes.byref(shape), int(Is), ctypes.byref(lora), *args, ws, nbytes,
-                                   _stream(stream)), "moe_shared_ffn_lora")
+    T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
+    L, n = lora.adapters, lora.adapters * lora.rank
+    _check(lib.moe_shared_ffn_lora(
+        ctypes.byref(shape), Is, ctypes.byref(lora), _on(here, "x", x, dt, T * H), _on(here, "w1s", w1s, dt, 2 * Is * H),
+        _on(here, "w2s", w2s, dt, H * Is), _on(here, "a1", a1, dt, n * H), _on(here, "b1", b1, dt, n * 2 * Is),
+        _on(here, "a2", a2, dt, n * Is), _on(here, "b2", b2, dt, n * H), _on(here, "scale", scale, torch.float32, L),
+        _on(here, "adapter_ids", adapter_ids, torch.int32, T), _on(here, "residual", residual, dt, T * H, True),
+        _on(here, "hs", hs, dt, T * Is), _on(here, "out", out, dt, T * H), *_workspace_on(here, workspace),
+        _stream_on(here, stream)), "moe_shared_ffn_lora")
 
 
 def moe_probe_mfma_bf16(iterations: int, sink, stream=None) -> float:

@@ -419,6 +419,22 @@ hipError_t big(const Ffn& f, const Lora& l, const void* x, int K, const void* w,
 // ---------------------------------------------------------------------------
 // Up to kSmallTokens tokens.
 
+// One row of A times x over the 8-column chunks c0 .. c1, by a wave.
+__device__ __forceinline__ float low_rank_value(const uint16_t* x, const uint16_t* a, int c0, int c1, int lane) {
+  float s = 0.0f;
+#pragma unroll 4
+  for (int c = c0 + lane; c < c1; c += 64) {
+    tile::Vec8<uint16_t> p, q;
+    p.load(x + c * 8);
+    q.load(a + c * 8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(p[e], q[e], s);
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  return s;
+}
+
 // v[part, t, j] = s_a A_a[j] . x[t] over a part of K, a wave for each.
 __global__ __launch_bounds__(256) void shrink_small(const uint16_t* x, const uint16_t* a, const float* scale,
                                                     const int32_t* ids, int T, int K, int L, int r, int parts,
@@ -429,18 +445,8 @@ __global__ __launch_bounds__(256) void shrink_small(const uint16_t* x, const uin
   if (ad < 0 || ad >= L) return;
   const int chunks = K / 8;
   const int c0 = chunks * part / parts, c1 = chunks * (part + 1) / parts;
-  const float sc = scale[ad];
-  float s = 0.0f;
-  for (int c = c0 + lane; c < c1; c += 64) {
-    tile::Vec8<uint16_t> p, q;
-    p.load(x + (size_t)t * K + c * 8);
-    q.load(a + ((size_t)ad * r + j) * K + c * 8);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(p[e], q[e], s);
-  }
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-  if (lane == 0) v[((size_t)part * T + t) * r + j] = s * sc;
+  const float s = low_rank_value(x + (size_t)t * K, a + ((size_t)ad * r + j) * K, c0, c1, lane);
+  if (lane == 0) v[((size_t)part * T + t) * r + j] = s * scale[ad];
 }
 
 // ROWS rows of W (PAIR: half of them gate rows, then their up rows), all
@@ -451,9 +457,11 @@ __global__ __launch_bounds__(256) void shrink_small(const uint16_t* x, const uin
 // behind the first copies, so that the latencies overlap.
 constexpr int kStreamWaves = 16, kStreamRing = 2;
 
-template <bool PAIR, int ROWS>
+// OWN: the low-rank values are computed here, by every workgroup for itself.
+template <bool PAIR, int ROWS, bool OWN>
 __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(const uint16_t* x, const uint16_t* w,
-                                                                   const uint16_t* b, const int32_t* ids,
+                                                                   const uint16_t* a, const uint16_t* b,
+                                                                   const float* scale, const int32_t* ids,
                                                                    const float* v, const uint16_t* residual,
                                                                    uint16_t* out, int T, int K, int N, int L, int r,
                                                                    int parts) {
@@ -508,12 +516,22 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(const uint16_
     for (int c = 0; c < 4; ++c)
       if (c * 8 < r) q[c].load(pb + c * 8);
   }
-  for (int e = tid; e < T * r; e += kStreamWaves * 64) {
-    const int a = ids[e / r];
-    float s = 0.0f;
-    if (a >= 0 && a < L)
-      for (int p = 0; p < parts; ++p) s += v[(size_t)p * T * r + e];
-    low[e] = s;
+  if constexpr (OWN) {
+    for (int e = wave; e < T * r; e += kStreamWaves) {
+      const int to = e / r, id = ids[to];
+      if (id >= 0 && id < L) {
+        const float s = low_rank_value(x + (size_t)to * K, a + ((size_t)id * r + e % r) * K, 0, K / 8, lane) * scale[id];
+        if (lane == 0) low[e] = s;
+      }
+    }
+  } else {
+    for (int e = tid; e < T * r; e += kStreamWaves * 64) {
+      const int id = ids[e / r];
+      float s = 0.0f;
+      if (id >= 0 && id < L)
+        for (int p = 0; p < parts; ++p) s += v[(size_t)p * T * r + e];
+      low[e] = s;
+    }
   }
 
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -580,18 +598,26 @@ hipError_t small(const Ffn& f, const Lora& l, const void* x, int K, const void* 
                  hipStream_t st) {
   const Space s = space(f, l, ws);
   const int parts = parts_of(f, K);
-  hipLaunchKernelGGL(shrink_small, dim3(f.T, parts, l.r / 4), dim3(256), 0, st, (const uint16_t*)x,
-                     (const uint16_t*)a, scale, ids, f.T, K, l.L, l.r, parts, s.v);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  // Few low-rank values: every workgroup computes them for itself (two rows of A
+  // a wave at most, from L2), which costs less than a launch.  One token,
+  // rank 16, both projections: 12 us of kernels in two launches, 15 us in four (a
+  // pass among others 16 and 24 us).
+  const bool own = f.T * l.r <= 2 * kStreamWaves;
+  if (!own) {
+    hipLaunchKernelGGL(shrink_small, dim3(f.T, parts, l.r / 4), dim3(256), 0, st, (const uint16_t*)x,
+                       (const uint16_t*)a, scale, ids, f.T, K, l.L, l.r, parts, s.v);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   auto stream = [&](auto kernel, int per) {
     hipLaunchKernelGGL(kernel, dim3(rows / per), dim3(kStreamWaves * 64), 0, st, (const uint16_t*)x,
-                       (const uint16_t*)w, (const uint16_t*)b, ids, s.v, (const uint16_t*)residual, (uint16_t*)out,
-                       f.T, K, rows, l.L, l.r, parts);
+                       (const uint16_t*)w, (const uint16_t*)a, (const uint16_t*)b, scale, ids, s.v,
+                       (const uint16_t*)residual, (uint16_t*)out, f.T, K, rows, l.L, l.r, parts);
     return hipGetLastError();
   };
   // sixteen rows a workgroup leave CUs without one below 4096 rows
-  return rows < 4096 ? stream(stream_kernel<PAIR, 8>, 8) : stream(stream_kernel<PAIR, 16>, 16);
+  if (rows < 4096) return own ? stream(stream_kernel<PAIR, 8, true>, 8) : stream(stream_kernel<PAIR, 8, false>, 8);
+  return own ? stream(stream_kernel<PAIR, 16, true>, 16) : stream(stream_kernel<PAIR, 16, false>, 16);
 }
 
 }  // namespace

@@ -32,11 +32,12 @@ constexpr int kMaxParts = 8;
 bool small_path(const Ffn& f) { return f.bf16 && f.T <= kSmallTokens; }
 
 // Parts of K whose low-rank sums are kept apart, so that few tokens still
-// spread over the chip: 512 workgroups, at least 512 columns a part.
+// spread over the chip: 512 workgroups, at least 128 columns a part (512 where
+// a wave takes a row of A by itself).
 int parts_of(const Ffn& f, int K) {
-  const int units = small_path(f) ? 1 : (f.T + 31) / 32;
+  const int units = small_path(f) ? 1 : (f.T + 31) / 32, least = small_path(f) ? 512 : 128;
   int p = 512 / units;
-  p = p < K / 512 ? p : K / 512;
+  p = p < K / least ? p : K / least;
   return p < 1 ? 1 : p > kMaxParts ? kMaxParts : p;
 }
 

@@ -5,10 +5,12 @@
 //   d_x = [dg|du] w1,  d_w1 = [dg|du]^T x,  d_w2 = d_out^T h
 //
 // The weights are read as k-rows by the products that run back through them,
-// x, h, d_out and dg|du by the weights' gradients: no transposed copies.  The
-// three products of the second line do not depend on each other; they share a
-// launch, whose tiles of the longest sums go first, so that the chip is left
-// half idle once and not three times.
+// x, h, d_out and dg|du by the weights' gradients: no transposed copies.  Each
+// launch holds a product over the tokens' rows and a weight's gradient that
+// does not wait for it (dg|du and d_w2, then d_x and d_w1), the longer sums
+// first: the chip is left half idle twice and not four times, and the first
+// product's epilogue, bound by memory (it reads g and u), runs beside the
+// other's matrix work.
 #include "shared_train.h"
 #include "tile_gemm.h"
 
@@ -54,96 +56,104 @@ struct SwigluBackward {
   }
 };
 
-template <class E>
-hipError_t dgu(const Ffn& f, const Dropout& d, const void* d_out, const void* w2, const void* gu, void* d_gu,
-               hipStream_t st) {
-  return tile::run_product<E, false, true>(Operand{d_out, f.H, f.T}, Operand{w2, f.I, f.I}, f.H, 0,
-                                           SwigluBackward<E>{(const float*)gu, (E*)d_gu, f.I, d}, st);
-}
-
+// A product over rows of tokens (A k-contiguous, B k-rows), and a weight's
+// gradient (both k-rows).
 struct Part {
   Operand A, B;
   int K, mt, nt;
-  void* out;
-};
-struct Parts {
-  Part p[3];
-  int dx;  // which of them is d_x (its A is k-contiguous; -1: none of them)
 };
 
-// Each die takes an eighth of every part, parts in order.
-template <class CX, class CW>
-__global__ __launch_bounds__(CX::NTHR, 1) void gradients_kernel(Parts parts) {
-  typedef typename CX::E E;
+// Each die takes an eighth of either part's tiles, one part after the other.
+template <class CX, class CW, class Epi>
+__global__ __launch_bounds__(CX::NTHR, 1) void gradients_kernel(Part x, Part w, bool w_first, Epi epi_x,
+                                                                tile::StoreOut<typename CX::E> epi_w) {
   static_assert(CX::LDS_BYTES == CW::LDS_BYTES && CX::NTHR == CW::NTHR && CX::BM == CW::BM && CX::BN == CW::BN, "one tile size");
   __shared__ __attribute__((aligned(1024))) char smem[CX::LDS_BYTES];
-  int slot = blockIdx.x / kXcds;
-#pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    const Part& p = parts.p[i];
-    const int all = p.mt * p.nt, per = (all + kXcds - 1) / kXcds;
-    if (slot < per) {
-      const int t = (blockIdx.x % kXcds) * per + slot;
-      if (t >= all) return;
-      int tm, tn;
-      tile::tile_of(t, p.mt, p.nt, tm, tn);
-      const tile::StoreOut<E> epi{(E*)p.out, nullptr, p.B.count};
-      if (i == parts.dx)
-        tile::product<CX>(p.A, p.B, p.K, 0, tm * CX::BM, tn * CX::BN, epi, tile::NoExtra{}, smem);
-      else
-        tile::product<CW>(p.A, p.B, p.K, 0, tm * CW::BM, tn * CW::BN, epi, tile::NoExtra{}, smem);
-      return;
-    }
-    slot -= per;
+  const int die = blockIdx.x % kXcds, slot = blockIdx.x / kXcds;
+  const int all_x = x.mt * x.nt, all_w = w.mt * w.nt, per_x = (all_x + kXcds - 1) / kXcds, per_w = (all_w + kXcds - 1) / kXcds;
+  const bool is_w = w_first ? slot < per_w : slot >= per_x;
+  int tm, tn;
+  if (is_w) {
+    const int s = w_first ? slot : slot - per_x, t = die * per_w + s;
+    if (t >= all_w) return;
+    tile::tile_of(t, w.mt, w.nt, tm, tn);
+    tile::product<CW>(w.A, w.B, w.K, 0, tm * CW::BM, tn * CW::BN, epi_w, tile::NoExtra{}, smem);
+  } else {
+    const int s = w_first ? slot - per_w : slot, t = die * per_x + s;
+    if (t >= all_x) return;
+    tile::tile_of(t, x.mt, x.nt, tm, tn);
+    tile::product<CX>(x.A, x.B, x.K, 0, tm * CX::BM, tn * CX::BN, epi_x, tile::NoExtra{}, smem);
   }
 }
 
-template <class E>
-hipError_t gradients(const Ffn& f, const void* x, const void* w1, const void* hs, const void* d_out, const void* d_gu,
-                     void* d_x, void* d_w1, void* d_w2, hipStream_t st) {
-  Part dx{Operand{d_gu, 2 * f.I, f.T}, Operand{w1, f.H, f.H}, 2 * f.I, 0, 0, d_x};
-  Part a{Operand{d_gu, 2 * f.I, 2 * f.I}, Operand{x, f.H, f.H}, f.T, 0, 0, d_w1};
-  Part b{Operand{d_out, f.H, f.H}, Operand{hs, f.I, f.I}, f.T, 0, 0, d_w2};
-  Parts q = dx.K > f.T ? Parts{{dx, a, b}, 0} : Parts{{a, b, dx}, 2};
+// Estimated ns until `n1` tiles of `a` ns and behind them `n2` of `b` ns are
+// done, every tile going to the place that is free first.
+long long makespan(long long n1, long long a, long long n2, long long b, long long places) {
+  // the places that hold one tile of the first kind more, and the others
+  const long long extra = n1 % places;
+  long long t_extra = (n1 / places + 1) * a, t = n1 / places * a;
+  while (n2 > 0) {
+    const bool e = extra > 0 && t_extra <= t;
+    (e ? t_extra : t) += b;
+    n2 -= e ? extra : places - extra;
+  }
+  return extra > 0 && t_extra > t ? t_extra : t;
+}
+
+// has_x, has_w: which of the two are wanted.
+template <class E, class Epi>
+hipError_t run_both(Part x, bool has_x, const Epi& epi_x, Part w, bool has_w, const tile::StoreOut<E>& epi_w,
+                    hipStream_t st) {
   const int size = tile::cheapest<E>([&](const tile::TileCost& c) {
-    // the tiles' time spread over the chip, and half a tile of the longest sum for the last round
-    long long sum = 0, longest = 0;
-    for (const Part& p : q.p) {
-      if (p.out == nullptr) continue;
-      const long long tiles = (long long)((p.A.count + c.bm - 1) / c.bm) * ((p.B.count + c.bn - 1) / c.bn);
-      const long long steps = ((long long)p.K * sizeof(E) + 127) / 128;
-      sum += tiles * tile::tile_ns(c, steps, c.resident) / c.resident;
-      const long long one = tile::tile_ns(c, steps, 1);
-      longest = longest > one ? longest : one;
-    }
-    const long long spread = sum / tile::kCus;
-    return spread > longest / 2 ? spread + longest / 2 : longest;
+    auto tiles = [&](const Part& p, bool has) {
+      return has ? (long long)((p.A.count + c.bm - 1) / c.bm) * ((p.B.count + c.bn - 1) / c.bn) : 0;
+    };
+    const long long nx = tiles(x, has_x), nw = tiles(w, has_w), a_cu = (nx + nw + tile::kCus - 1) / tile::kCus;
+    const int resident = a_cu < 1 ? 1 : a_cu < c.resident ? (int)a_cu : c.resident;
+    auto ns = [&](const Part& p) { return tile::tile_ns(c, ((long long)p.K * sizeof(E) + 127) / 128, resident); };
+    return w.K > x.K ? makespan(nw, ns(w), nx, ns(x), tile::kCus * resident)
+                     : makespan(nx, ns(x), nw, ns(w), tile::kCus * resident);
   });
   return tile::with_tile<E>(size, [&](auto index) {
     typedef typename tile::TileCfg<E, decltype(index)::value, false, true>::type CX;
     typedef typename tile::TileCfg<E, decltype(index)::value, true, true>::type CW;
     unsigned slots = 0;
-    for (Part& p : q.p) {
-      if (p.out == nullptr) continue;
-      p.mt = (p.A.count + CX::BM - 1) / CX::BM;
+    auto split = [&](Part& p, bool has) {
+      p.mt = has ? (p.A.count + CX::BM - 1) / CX::BM : 0;
       p.nt = (p.B.count + CX::BN - 1) / CX::BN;
       slots += (unsigned)(((long long)p.mt * p.nt + kXcds - 1) / kXcds);
-    }
-    hipLaunchKernelGGL((gradients_kernel<CX, CW>), dim3(slots * kXcds), dim3(CX::NTHR), 0, st, q);
+    };
+    split(x, has_x);
+    split(w, has_w);
+    if (slots == 0) return hipSuccess;
+    hipLaunchKernelGGL((gradients_kernel<CX, CW, Epi>), dim3(slots * kXcds), dim3(CX::NTHR), 0, st, x, w, w.K > x.K,
+                       epi_x, epi_w);
     return hipGetLastError();
   });
 }
 
+template <class E>
+hipError_t backward(const Ffn& f, const Dropout& d, const void* x, const void* w1, const void* w2, const void* gu,
+                    const void* hs, const void* d_out, void* d_gu, void* d_x, void* d_w1, void* d_w2, hipStream_t st) {
+  const bool w = d_w1 != nullptr;
+  const hipError_t e = run_both<E>(Part{Operand{d_out, f.H, f.T}, Operand{w2, f.I, f.I}, f.H, 0, 0}, true,
+                                   SwigluBackward<E>{(const float*)gu, (E*)d_gu, f.I, d},
+                                   Part{Operand{d_out, f.H, f.H}, Operand{hs, f.I, f.I}, f.T, 0, 0}, w,
+                                   tile::StoreOut<E>{(E*)d_w2, nullptr, f.I}, st);
+  if (e != hipSuccess) return e;
+  return run_both<E>(Part{Operand{d_gu, 2 * f.I, f.T}, Operand{w1, f.H, f.H}, 2 * f.I, 0, 0}, d_x != nullptr,
+                     tile::StoreOut<E>{(E*)d_x, nullptr, f.H},
+                     Part{Operand{d_gu, 2 * f.I, 2 * f.I}, Operand{x, f.H, f.H}, f.T, 0, 0}, w,
+                     tile::StoreOut<E>{(E*)d_w1, nullptr, f.H}, st);
+}
+
 }  // namespace
 
-hipError_t launch_train_dgu(const Ffn& f, const Dropout& d, const void* d_out, const void* w2, const void* gu,
-                            void* d_gu, hipStream_t st) {
-  return f.bf16 ? dgu<uint16_t>(f, d, d_out, w2, gu, d_gu, st) : dgu<float>(f, d, d_out, w2, gu, d_gu, st);
-}
-hipError_t launch_train_gradients(const Ffn& f, const void* x, const void* w1, const void* hs, const void* d_out,
-                                  const void* d_gu, void* d_x, void* d_w1, void* d_w2, hipStream_t st) {
-  return f.bf16 ? gradients<uint16_t>(f, x, w1, hs, d_out, d_gu, d_x, d_w1, d_w2, st)
-                : gradients<float>(f, x, w1, hs, d_out, d_gu, d_x, d_w1, d_w2, st);
+hipError_t launch_train_backward(const Ffn& f, const Dropout& d, const void* x, const void* w1, const void* w2,
+                                 const void* gu, const void* hs, const void* d_out, void* d_gu, void* d_x, void* d_w1,
+                                 void* d_w2, hipStream_t st) {
+  return f.bf16 ? backward<uint16_t>(f, d, x, w1, w2, gu, hs, d_out, d_gu, d_x, d_w1, d_w2, st)
+                : backward<float>(f, d, x, w1, w2, gu, hs, d_out, d_gu, d_x, d_w1, d_w2, st);
 }
 
 }  // namespace moe

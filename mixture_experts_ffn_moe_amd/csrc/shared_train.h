@@ -19,13 +19,12 @@ hipError_t launch_train_w13(const Ffn& f, const Dropout& d, const void* x, const
 // out [T, H] = hs w2^T (+ residual)
 hipError_t launch_train_down(const Ffn& f, const void* hs, const void* w2, const void* residual, void* out,
                              hipStream_t st);
-// d_gu [T, 2I] from d_out w2, gu and the dropout
-hipError_t launch_train_dgu(const Ffn& f, const Dropout& d, const void* d_out, const void* w2, const void* gu,
-                            void* d_gu, hipStream_t st);
-// d_x [T, H] = d_gu w1, d_w1 [2I, H] = d_gu^T x and d_w2 [H, I] = d_out^T hs; d_x,
-// or d_w1 and d_w2, may be null (not wanted).  T == 0: d_w1 and d_w2 are zeros.
-hipError_t launch_train_gradients(const Ffn& f, const void* x, const void* w1, const void* hs, const void* d_out,
-                                  const void* d_gu, void* d_x, void* d_w1, void* d_w2, hipStream_t st);
+// d_gu [T, 2I] from d_out w2, gu and the dropout; d_x [T, H] = d_gu w1,
+// d_w1 [2I, H] = d_gu^T x and d_w2 [H, I] = d_out^T hs; d_x, or d_w1 and d_w2, may
+// be null (not wanted).  T == 0: d_w1 and d_w2 are zeros.
+hipError_t launch_train_backward(const Ffn& f, const Dropout& d, const void* x, const void* w1, const void* w2,
+                                 const void* gu, const void* hs, const void* d_out, void* d_gu, void* d_x, void* d_w1,
+                                 void* d_w2, hipStream_t st);
 
 // out = residual (may be null) + dropout(y), n elements, n a multiple of 8
 hipError_t launch_dropout(bool bf16, const Dropout& d, long long n, const void* y, const void* residual, void* out,

@@ -206,7 +206,7 @@ __device__ __forceinline__ void settle() {
 // Tile t of mt x nt: tiles run down groups of 8 row tiles, so that the 32
 // tiles a die works on at a time share their rows and columns in its L2.
 __device__ __forceinline__ void tile_of(int t, int mt, int nt, int& m, int& n) {
-  constexpr int G = 8;
+  constexpr int G = 4;
   const int group = t / (G * nt), in = t - group * (G * nt);
   const int rows = min(G, mt - group * G);
   m = group * G + in % rows;
@@ -469,8 +469,8 @@ struct TileCosts;
 template <>
 struct TileCosts<uint16_t> {
   static constexpr int COUNT = 6;
-  static constexpr TileCost C[COUNT] = {{32, 64, 3, {185, 310, 460}}, {64, 64, 2, {210, 370, 0}}, {64, 128, 1, {305, 0, 0}},
-                                        {128, 128, 1, {490, 0, 0}},   {128, 256, 1, {900, 0, 0}}, {256, 256, 1, {1630, 0, 0}}};
+  static constexpr TileCost C[COUNT] = {{32, 64, 3, {185, 290, 420}}, {64, 64, 2, {230, 400, 0}}, {64, 128, 1, {340, 0, 0}},
+                                        {128, 128, 1, {490, 0, 0}},   {128, 256, 1, {880, 0, 0}}, {256, 256, 1, {1630, 0, 0}}};
 };
 template <>
 struct TileCosts<float> {
@@ -492,7 +492,7 @@ template <bool TA, bool TB> struct TileCfg<float, 2, TA, TB> { typedef Cfg<float
 template <bool TA, bool TB> struct TileCfg<float, 3, TA, TB> { typedef Cfg<float, 128, 128, 2, 4, 16, 128, 4, TA, TB> type; };
 
 inline long long tile_ns(const TileCost& c, long long steps, int resident) {
-  return steps * c.step[resident - 1] + 1500 + c.bm * c.bn / 10;
+  return steps * c.step[resident - 1] + 2200 + c.bm * c.bn / 8;
 }
 constexpr int kCus = 256;
 // Estimated ns of an M x N product: whole rounds of `resident` tiles a CU, and

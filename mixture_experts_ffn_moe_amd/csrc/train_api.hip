@@ -116,18 +116,15 @@ moe_status moe_shared_ffn_backward(const moe_shape* shape, int32_t Is, double p,
   MOE_CHECK(check_dropout(p, rng, &d));
   if ((d_w1s == nullptr) != (d_w2s == nullptr) || (d_x == nullptr && d_w1s == nullptr)) return MOE_ERR_INVALID_ARG;
   MOE_CHECK(check_or_null(d_x)); MOE_CHECK(check_or_null(d_w1s)); MOE_CHECK(check_or_null(d_w2s));
-  hipStream_t st = (hipStream_t)stream;
   if (f.T > 0) {
     if (d_w1s) MOE_CHECK(check_ptr(x));
     if (d_w1s) MOE_CHECK(check_ptr(hs));
     if (d_x) MOE_CHECK(check_ptr(w1s));
     MOE_CHECK(check_ptr(w2s)); MOE_CHECK(check_ptr(gu)); MOE_CHECK(check_ptr(d_out));
     MOE_CHECK(check_workspace(workspace, workspace_bytes, backward_bytes(f)));
-    MOE_CHECK(hip_status(moe::launch_train_dgu(f, d, d_out, w2s, gu, workspace, st)));
-  } else if (d_w1s == nullptr) {
-    return MOE_OK;
   }
-  return hip_status(moe::launch_train_gradients(f, x, w1s, hs, d_out, workspace, d_x, d_w1s, d_w2s, st));
+  return hip_status(moe::launch_train_backward(f, d, x, w1s, w2s, gu, hs, d_out, workspace, d_x, d_w1s, d_w2s,
+                                               (hipStream_t)stream));
 }
 
 size_t moe_lora_workspace_size(const moe_shape* shape, int32_t Is, const moe_lora_spec* spec) {

@@ -21,4 +21,4 @@ from ._lib import (  # noqa: F401
     moe_shared_backward_workspace_size, moe_shared_ffn, moe_shared_ffn_backward, moe_shared_ffn_lora,
     moe_shared_ffn_train, moe_shared_workspace_size, moe_workspace_size, status_string, y_nbytes,
 )
-from .layer import MoELayerBuffers, workspace_views  # noqa: F401
+from .layer import MoELayerBuffers, SharedTrainBuffers, workspace_views  # noqa: F401

@@ -595,7 +595,7 @@ def moe_dropout_backward(shape, p, rng, d_out, d_y, stream=None):
 def moe_shared_ffn_train(shape, Is, p, rng, x, w1s, w2s, residual, gu, hs, out, stream=None):
     """The shared expert's forward pass with dropout of its hidden values; keeps gu (fp32) and hs for the backward pass."""
     T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
-    _check(lib.moe_shared_ffn_train(ctypes.byref(shape), Is, p, _rng_on(here, p, rng), _on(here, "x", x, dt, T * H),
+    _check(lib.moe_shared_ffn_train(ctypes.byref(shape), int(Is), p, _rng_on(here, p, rng), _on(here, "x", x, dt, T * H),
                                     _on(here, "w1s", w1s, dt, 2 * Is * H), _on(here, "w2s", w2s, dt, H * Is),
                                     _on(here, "residual", residual, dt, T * H, True),
                                     _on(here, "gu", gu, torch.float32, T * 2 * Is), _on(here, "hs", hs, dt, T * Is),
@@ -611,7 +611,7 @@ def moe_shared_ffn_backward(shape, Is, p, rng, x, w1s, w2s, gu, hs, d_out, d_x, 
     T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
     no_x, no_w = d_x is None, d_w1s is None and d_w2s is None
     _check(lib.moe_shared_ffn_backward(
-        ctypes.byref(shape), Is, p, _rng_on(here, p, rng), _on(here, "x", x, dt, T * H, no_w),
+        ctypes.byref(shape), int(Is), p, _rng_on(here, p, rng), _on(here, "x", x, dt, T * H, no_w),
         _on(here, "w1s", w1s, dt, 2 * Is * H, no_x), _on(here, "w2s", w2s, dt, H * Is),
         _on(here, "gu", gu, torch.float32, T * 2 * Is), _on(here, "hs", hs, dt, T * Is, no_w),
         _on(here, "d_out", d_out, dt, T * H), _on(here, "d_x", d_x, dt, T * H, True),
@@ -636,7 +636,7 @@ def moe_lora_w13_swiglu(shape, Is, lora, x, w1s, a1, b1, scale, adapter_ids, hs,
     T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
     L, n = lora.adapters, lora.adapters * lora.rank
     _check(lib.moe_lora_w13_swiglu(
-        ctypes.byref(shape), Is, ctypes.byref(lora), _on(here, "x", x, dt, T * H), _on(here, "w1s", w1s, dt, 2 * Is * H),
+        ctypes.byref(shape), int(Is), ctypes.byref(lora), _on(here, "x", x, dt, T * H), _on(here, "w1s", w1s, dt, 2 * Is * H),
         _on(here, "a1", a1, dt, n * H), _on(here, "b1", b1, dt, n * 2 * Is), _on(here, "scale", scale, torch.float32, L),
         _on(here, "adapter_ids", adapter_ids, torch.int32, T), _on(here, "hs", hs, dt, T * Is), *_workspace_on(here, workspace),
         _stream_on(here, stream)), "moe_lora_w13_swiglu")
@@ -647,7 +647,7 @@ def moe_lora_down(shape, Is, lora, hs, w2s, a2, b2, scale, adapter_ids, residual
     T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
     L, n = lora.adapters, lora.adapters * lora.rank
     _check(lib.moe_lora_down(
-        ctypes.byref(shape), Is, ctypes.byref(lora), _on(here, "hs", hs, dt, T * Is), _on(here, "w2s", w2s, dt, H * Is),
+        ctypes.byref(shape), int(Is), ctypes.byref(lora), _on(here, "hs", hs, dt, T * Is), _on(here, "w2s", w2s, dt, H * Is),
         _on(here, "a2", a2, dt, n * Is), _on(here, "b2", b2, dt, n * H), _on(here, "scale", scale, torch.float32, L),
         _on(here, "adapter_ids", adapter_ids, torch.int32, T), _on(here, "residual", residual, dt, T * H, True),
         _on(here, "out", out, dt, T * H), *_workspace_on(here, workspace), _stream_on(here, stream)), "moe_lora_down")
@@ -659,7 +659,7 @@ def moe_shared_ffn_lora(shape, Is, lora, x, w1s, w2s, a1, b1, a2, b2, scale, ada
     T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
     L, n = lora.adapters, lora.adapters * lora.rank
     _check(lib.moe_shared_ffn_lora(
-        ctypes.byref(shape), Is, ctypes.byref(lora), _on(here, "x", x, dt, T * H), _on(here, "w1s", w1s, dt, 2 * Is * H),
+        ctypes.byref(shape), int(Is), ctypes.byref(lora), _on(here, "x", x, dt, T * H), _on(here, "w1s", w1s, dt, 2 * Is * H),
         _on(here, "w2s", w2s, dt, H * Is), _on(here, "a1", a1, dt, n * H), _on(here, "b1", b1, dt, n * 2 * Is),
         _on(here, "a2", a2, dt, n * Is), _on(here, "b2", b2, dt, n * H), _on(here, "scale", scale, torch.float32, L),
         _on(here, "adapter_ids", adapter_ids, torch.int32, T), _on(here, "residual", residual, dt, T * H, True),

@@ -106,9 +106,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count(const int32_t* ids, i
   for (int i = threadIdx.x; i <= L; i += kPlanThreads) hist[(size_t)blockIdx.x * (L + 1) + i] = bins[i];
 }
 
-// Every workgroup finds its first position in every bin from all counts, then
-// places its chunk.  Block 0 writes the bins' first positions.  A lone
-// workgroup (blocks == 1) counts by itself and reads no hist.
+// Every workgroup counts its chunk, finds its first position in every bin from
+// all chunks' counts (hist; a lone workgroup's are its own), and places its
+// tokens.  Block 0 writes the bins' first positions.
 __global__ __launch_bounds__(kPlanThreads) void plan_place(const int32_t* ids, int T, int L, int chunk,
                                                            const int32_t* hist, int blocks, int32_t* perm,
                                                            int32_t* sorted, int32_t* first) {
@@ -118,19 +118,17 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place(const int32_t* ids, i
   constexpr int KEEP = kPlanChunk / kPlanThreads;  // a thread's tokens of a chunk
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int t0 = blockIdx.x * chunk, t1 = min(T, t0 + chunk);
-  int bins[KEEP];
+  int bin[KEEP], place[KEEP];
 #pragma unroll
   for (int q = 0; q < KEEP; ++q) {
     const int t = t0 + q * kPlanThreads + threadIdx.x;
-    bins[q] = t < t1 ? bin_of(ids[t], L) : -1;
+    bin[q] = t < t1 ? bin_of(ids[t], L) : -1;
   }
+  for (int i = threadIdx.x; i <= L; i += kPlanThreads) start[i] = 0;
   if (threadIdx.x == 0) carry = 0;
-  if (blocks == 1) {
-    for (int i = threadIdx.x; i <= L; i += kPlanThreads) start[i] = 0;
-    __syncthreads();
+  __syncthreads();
 #pragma unroll
-    for (int q = 0; q < KEEP; ++q) count_up(start, bins[q], bins[q] >= 0);
-  }
+  for (int q = 0; q < KEEP; ++q) place[q] = count_up(start, bin[q], bin[q] >= 0);
   __syncthreads();
   for (int i0 = 0; i0 <= L; i0 += kPlanThreads) {
     const int i = i0 + threadIdx.x;
@@ -165,13 +163,12 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place(const int32_t* ids, i
   }
   if (blockIdx.x == 0 && threadIdx.x == 0) first[L + 1] = T;
 #pragma unroll
-  for (int q = 0; q < KEEP; ++q) {
-    const int at = count_up(start, bins[q], bins[q] >= 0);
-    if (bins[q] >= 0) {
+  for (int q = 0; q < KEEP; ++q)
+    if (bin[q] >= 0) {
+      const int at = start[bin[q]] + place[q];
       perm[at] = t0 + q * kPlanThreads + threadIdx.x;
-      sorted[at] = bins[q];
+      sorted[at] = bin[q];
     }
-  }
 }
 
 // ---------------------------------------------------------------------------
@@ -291,21 +288,23 @@ struct AddLora {
   }
 
   // Adds B_a v to the tile's accumulators, the ring's LDS in use for it: the
-  // tile's low-rank values of RS ranks (summed over the parts and rounded to
-  // the layer's type as the matrix operand they are), and a ring of the B rows
-  // of the tile's adapters, copied ahead.  b_r0(j): first tile row of this
+  // tile's low-rank values of RS ranks (summed over the parts), and a ring of
+  // the B rows of the tile's adapters, copied ahead.  In bf16 a low-rank value is
+  // the sum of two operands, its rounding and the rounding of what is left:
+  // rounded once it raised the error of SwiGLU's output from 1.7e-3 (its own
+  // rounding) to 3.1e-3 where the adapters' part is large.  b_r0(j): first tile row of this
   // wave's fragment j; brow(i): row of B of tile row i.
   template <class C, class R0, class Row>
   __device__ __forceinline__ void add(typename C::M::acc (&acc)[C::FM][C::FN], char* smem, int m0, int wave_m, R0 b_r0,
                                       Row brow, int wave, int lane) const {
     typedef Cfg<E, C::BM, C::BN, C::WM, C::WN, C::F, 128, 2, false, false> S;  // tiles of 128-byte rows
-    constexpr int RS = 128 / sizeof(E);
-    constexpr int RING = (C::LDS_BYTES - S::A_BYTES) / S::B_BYTES < 6 ? (C::LDS_BYTES - S::A_BYTES) / S::B_BYTES : 6;
+    constexpr int RS = 128 / sizeof(E), V_BYTES = sizeof(E) == 2 ? 2 * S::A_BYTES : S::A_BYTES;
+    constexpr int RING = (C::LDS_BYTES - V_BYTES) / S::B_BYTES < 6 ? (C::LDS_BYTES - V_BYTES) / S::B_BYTES : 6;
     static_assert(RING >= 2 && (RING - 2) * S::BQ < 64, "ring of B tiles");
     const Runs<C::BM>& list = runs<C::BM>();
     const int count = __builtin_amdgcn_readfirstlane(list.count);
     if (count == 0) return;
-    const uint32_t lds = (uint32_t)(uintptr_t)smem + S::A_BYTES;
+    const uint32_t lds = (uint32_t)(uintptr_t)smem + V_BYTES;
     for (int k0 = 0; k0 < r; k0 += RS) {
       const int left = min(RS, r - k0);
       if (k0) __syncthreads();
@@ -334,8 +333,14 @@ struct AddLora {
           }
         char* to = smem + row * 128 + (c ^ tile::swz_row<128>(row)) * 16;
         if constexpr (sizeof(E) == 2) {
-          const uint2 lo = pack_bf16x4(t[0]), hi = pack_bf16x4(t[1]);
-          *reinterpret_cast<uint4*>(to) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+          const uint2 a0 = pack_bf16x4(t[0]), a1 = pack_bf16x4(t[1]);
+          tile::Vec8<uint16_t> a;
+          a.d = make_uint4(a0.x, a0.y, a1.x, a1.y);
+          *reinterpret_cast<uint4*>(to) = a.d;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) t[i >> 2][i & 3] -= a[i];
+          const uint2 l0 = pack_bf16x4(t[0]), l1 = pack_bf16x4(t[1]);
+          *reinterpret_cast<uint4*>(to + S::A_BYTES) = make_uint4(l0.x, l0.y, l1.x, l1.y);
         } else {
           *reinterpret_cast<f32x4*>(to) = t[0];
         }
@@ -345,7 +350,7 @@ struct AddLora {
         tile::slot_barrier();
         const int r0 = __builtin_amdgcn_readfirstlane(list.run[n]) >> 16, r1 = __builtin_amdgcn_readfirstlane(list.run[n + 1]) >> 16;
         copy();
-        const char* tb = smem + S::A_BYTES + (n % RING) * S::B_BYTES;
+        const char* tb = smem + V_BYTES + (n % RING) * S::B_BYTES;
 #pragma unroll
         for (int i = 0; i < C::FM; ++i) {
           const int f0 = wave_m + C::F * i;
@@ -358,10 +363,14 @@ struct AddLora {
           for (int ks = 0; ks * C::M::SUB < left; ++ks) {
             const int some = left - ks * C::M::SUB;
             const typename C::M::frag fv = tile::read_frag<S, false, C::BM>(smem, wave_m + C::F * i, ks, lane);
+            typename C::M::frag rest;
+            if constexpr (sizeof(E) == 2)
+              rest = tile::read_frag<S, false, C::BM>(smem + S::A_BYTES, wave_m + C::F * i, ks, lane);
 #pragma unroll
             for (int j = 0; j < C::FN; ++j) {
               typename C::M::frag fb = tile::read_frag<S, false, C::BN>(tb, b_r0(j), ks, lane);
               if (some < C::M::SUB) fb = tile::mask_k<S>(fb, some, lane);
+              if constexpr (sizeof(E) == 2) d[j] = C::M::mul(fb, rest, d[j]);
               d[j] = C::M::mul(fb, fv, d[j]);
             }
           }

@@ -89,7 +89,8 @@ def ffn(x, w1, w2, residual, d_out, factors, dtype):
 
 
 def projection(x, w, a, b, scale, ids, dtype, rounded):
-    """(value, bound) of x w^T plus each token's adapter; rounded: the low-rank values pass through dtype."""
+    """(value, bound) of x w^T plus each token's adapter; rounded: the low-rank values pass through two operands of
+    dtype, their rounding and the rounding of the rest (off by a half step of a half step)."""
     z, ez = _mm(x, w.T)
     for l in torch.unique(ids).tolist():
         if not 0 <= l < a.shape[0]:
@@ -98,7 +99,7 @@ def projection(x, w, a, b, scale, ids, dtype, rounded):
         v, ev = _mm(x[rows], a[l].T)
         v, ev = v * scale[l], (ev + 9 * F32 * v.abs()) * abs(scale[l])  # up to eight parts of K, then the scale
         if rounded:
-            ev = _stored(v, ev, dtype)
+            ev = ev + half_step(dtype) ** 2 * (v.abs() + ev)
         y, ey = _mm(v, b[l].T)
         z[rows] += y
         ez[rows] += ey + 1.02 * (ev @ b[l].abs().T) + F32 * (y.abs() + z[rows].abs())

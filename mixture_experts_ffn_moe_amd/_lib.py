@@ -550,8 +550,11 @@ def _here() -> int:
 
 def _on(here: int, name: str, t, dtype: torch.dtype, numel: int, nullable: bool = False):
     """_arg for a tensor that has to be on the current device."""
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.numel() == numel and t.get_device() == here and t.is_contiguous():
-        return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.numel() == numel and t.get_device() == here and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # no tensor: _arg says so
+        pass
     p = _arg(name, t, dtype, numel, nullable)
     if t is not None:
         _on_current(t)

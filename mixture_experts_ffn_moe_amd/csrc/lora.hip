@@ -41,7 +41,7 @@ int parts_of(const Ffn& f, int K) {
   return p < 1 ? 1 : p > kMaxParts ? kMaxParts : p;
 }
 
-// Tokens of a workgroup of the sort.
+// Tokens of a workgroup of the sort (8192 tokens in one workgroup: 8.4 us; 300: 3.9 us).
 constexpr int kPlanThreads = 1024, kPlanChunk = 8192;
 int plan_blocks(int T) { return (T + kPlanChunk - 1) / kPlanChunk; }
 
@@ -464,7 +464,9 @@ __global__ __launch_bounds__(256) void shrink_small(const uint16_t* x, const uin
 // own in LDS that direct copies fill with whole 128-byte rows (no workgroup
 // barrier); their sums meet in LDS, and a thread finishes one (token, row).
 // What the end needs (low-rank values, the first 32 ranks of B) is loaded right
-// behind the first copies, so that the latencies overlap.
+// behind the first copies, so that the latencies overlap.  16 tokens, H = 4096,
+// Is = 768, rank 32: 7.1 us for w13 (12.6 MB of weights, 2.7 us at the copy rate; 13 us
+// with operands read straight from memory, 16 rows per 16 lanes) and 4.5 us down.
 constexpr int kStreamWaves = 16, kStreamRing = 2;
 
 // OWN: the low-rank values are computed here, by every workgroup for itself.

@@ -18,6 +18,14 @@
 //     of one row m; the finished tile passes through LDS in strips of F rows
 //     per wave (the wave's own region: no workgroup barrier) and each lane
 //     finishes 8 consecutive columns with 16-byte loads and stores.
+//   * eight waves of 128 x 64 of a 256 x 256 tile (two a SIMD) rather than four of
+//     128 x 128 (one): 210 against 220 us for 8192 x 4096 x 4096 both
+//     k-contiguous (1.31 PFLOP/s), 204 against 216 us both k-rows; without copies
+//     170 us.  Copies and operand reads share LDS; the matrix pipe is busy 80 %
+//     of the CUs' cycles at sums of 4096 and 8192, 54 % at 2048, where what a
+//     tile does before and behind its sum (9 us a round) weighs more.
+//   * small tiles are bound by the copies: 32 x 64 move 29 (one workgroup a CU)
+//     to 40 bytes a clock and CU, the direct copies' limit.
 // Every row, column and k index that would lie outside an operand is clamped
 // to its last one; what was read for them is masked (k) or never stored.
 #pragma once

@@ -12,9 +12,10 @@
  * 16-byte aligned, contiguous row-major memory; `stream` is a hipStream_t
  * passed as void*; host-side validation first, and on any error nothing is
  * enqueued and no output is touched; T == 0 is valid and enqueues nothing.  Of
- * `shape`, T, H and dtype matter here (all fields are checked).  The same call
- * gives the same bits, and what a token gets depends on its own adapter's
- * values alone (others' may be NaN).  A workspace belongs to one call at a
+ * `shape`, T, H and dtype matter here (all fields are checked).  An output
+ * overlaps no input, except where it says so.  The same call gives the same
+ * bits, and what a token gets depends on its own adapter's values alone (others'
+ * may be NaN), not on the other tokens of a batch of as many.  A workspace belongs to one call at a
  * time: calls that may overlap (other streams, other captured graphs) need
  * their own.
  *

@@ -12,8 +12,9 @@
  * 16-byte aligned, contiguous row-major memory; `stream` is a hipStream_t
  * passed as void*; host-side validation first, and on any error nothing is
  * enqueued and no output is touched.  Of `shape`, T, H and dtype matter here
- * (all fields are checked).  Sums run in a fixed order: the same call gives
- * the same bits.  A workspace belongs to one call at a time: calls that may
+ * (all fields are checked).  An output overlaps no input and no other output,
+ * except where it says so.  Sums run in a fixed order: the same call gives the
+ * same bits.  A workspace belongs to one call at a time: calls that may
  * overlap (other streams, other captured graphs) need their own.
  *
  * Envelope, beside moe_mi355x.h's: Is % 32 == 0, 2*T*Is < 2^31, w1s below

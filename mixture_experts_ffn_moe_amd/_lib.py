@@ -583,7 +583,7 @@ def _rng_on(here: int, p, rng):
 def moe_dropout_add(shape, p, rng, y, residual, out, stream=None):
     """out = residual (or None) + dropout(y); rng: int64 [2] on the GPU, seed and offset."""
     n, dt, here = shape.T * shape.H, _layer_dtype(shape), _here()
-    _check(lib.moe_dropout_add(ctypes.byref(shape), p, _rng_on(here, p, rng), _on(here, "y", y, dt, n),
+    _check(lib.moe_dropout_add(ctypes.byref(shape), float(p), _rng_on(here, p, rng), _on(here, "y", y, dt, n),
                                _on(here, "residual", residual, dt, n, True), _on(here, "out", out, dt, n),
                                _stream_on(here, stream)), "moe_dropout_add")
 
@@ -591,14 +591,14 @@ def moe_dropout_add(shape, p, rng, y, residual, out, stream=None):
 def moe_dropout_backward(shape, p, rng, d_out, d_y, stream=None):
     """Gradient of moe_dropout_add's y, with the forward call's p and rng."""
     n, dt, here = shape.T * shape.H, _layer_dtype(shape), _here()
-    _check(lib.moe_dropout_backward(ctypes.byref(shape), p, _rng_on(here, p, rng), _on(here, "d_out", d_out, dt, n),
+    _check(lib.moe_dropout_backward(ctypes.byref(shape), float(p), _rng_on(here, p, rng), _on(here, "d_out", d_out, dt, n),
                                     _on(here, "d_y", d_y, dt, n), _stream_on(here, stream)), "moe_dropout_backward")
 
 
 def moe_shared_ffn_train(shape, Is, p, rng, x, w1s, w2s, residual, gu, hs, out, stream=None):
     """The shared expert's forward pass with dropout of its hidden values; keeps gu (fp32) and hs for the backward pass."""
     T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
-    _check(lib.moe_shared_ffn_train(ctypes.byref(shape), int(Is), p, _rng_on(here, p, rng), _on(here, "x", x, dt, T * H),
+    _check(lib.moe_shared_ffn_train(ctypes.byref(shape), int(Is), float(p), _rng_on(here, p, rng), _on(here, "x", x, dt, T * H),
                                     _on(here, "w1s", w1s, dt, 2 * Is * H), _on(here, "w2s", w2s, dt, H * Is),
                                     _on(here, "residual", residual, dt, T * H, True),
                                     _on(here, "gu", gu, torch.float32, T * 2 * Is), _on(here, "hs", hs, dt, T * Is),
@@ -614,7 +614,7 @@ def moe_shared_ffn_backward(shape, Is, p, rng, x, w1s, w2s, gu, hs, d_out, d_x, 
     T, H, dt, here = shape.T, shape.H, _layer_dtype(shape), _here()
     no_x, no_w = d_x is None, d_w1s is None and d_w2s is None
     _check(lib.moe_shared_ffn_backward(
-        ctypes.byref(shape), int(Is), p, _rng_on(here, p, rng), _on(here, "x", x, dt, T * H, no_w),
+        ctypes.byref(shape), int(Is), float(p), _rng_on(here, p, rng), _on(here, "x", x, dt, T * H, no_w),
         _on(here, "w1s", w1s, dt, 2 * Is * H, no_x), _on(here, "w2s", w2s, dt, H * Is),
         _on(here, "gu", gu, torch.float32, T * 2 * Is), _on(here, "hs", hs, dt, T * Is, no_w),
         _on(here, "d_out", d_out, dt, T * H), _on(here, "d_x", d_x, dt, T * H, True),

@@ -6,16 +6,17 @@
 // More than kSmallTokens tokens (or fp32):
 //   * plan: a counting sort of the tokens by adapter, tokens without one last
 //     (perm, the sorted adapters, every adapter's first position);
-//   * shrink: low-rank values v[position, :] = s_a A_a x, one workgroup for 32
-//     tokens of one adapter and a part of K, fp32 partial sums;
+//   * low-rank values v = s_a A_a x, fp32 partial sums over parts of K: by tiles of
+//     32 sorted tokens of one adapter (after the plan, v by position), or, few of
+//     them, by a wave for each (beside the plan in one launch, v by token);
 //   * product: the tiled product of tile_gemm.h over the sorted tokens, whose
 //     accumulators take B_a v before the epilogue.  A fragment of rows that
 //     several adapters share computes each one's product and every row takes
 //     its own: no other adapter's values, NaN or not, reach a row, and the
 //     order of tokens within an adapter does not change any bit.
-// Up to kSmallTokens tokens in bf16: no sort; shrink per token, then one
-// kernel that streams W with the tokens as the matrix instruction's columns
-// and adds B_a v in its epilogue.
+// Up to kSmallTokens tokens in bf16: no sort; a wave for each low-rank value,
+// then one kernel that streams W with the tokens as the matrix instruction's
+// columns and adds B_a v in its epilogue.
 #include "shared_train.h"
 #include "tile_gemm.h"
 
@@ -31,19 +32,29 @@ constexpr int kMaxParts = 8;
 
 bool small_path(const Ffn& f) { return f.bf16 && f.T <= kSmallTokens; }
 
+// Tokens of a workgroup of the sort (8192 tokens in one workgroup: 8.4 us; 300: 3.9 us).
+constexpr int kPlanThreads = 1024, kPlanChunk = 8192;
+int plan_blocks(int T) { return (T + kPlanChunk - 1) / kPlanChunk; }
+
+// Few low-rank values of short adapters are computed by a wave each: every wave
+// reads a row of A, from L2 mostly.  bf16, K = 4096, rank 16, a call of w13 by
+// waves and by tiles: 300 tokens 30.0 and 31.8 us (7.8 to 8.3 us with the sort in the
+// same launch; 4.8 and 5.3 in two), 512 tokens 36.0 and 39.0, 768 tokens 41.9 and 38.5;
+// rank 64, 128 tokens: 32.5 and 28.3.  fp32, K = 448, rank 8, 77 tokens: 13.2 and 18.5.
+bool by_wave(const Ffn& f, const Lora& l, int K) {
+  return small_path(f) || (f.T <= kPlanChunk && (long long)f.T * l.r <= 8192 && (long long)l.r * K <= 1 << 16);
+}
+
 // Parts of K whose low-rank sums are kept apart, so that few tokens still
-// spread over the chip: 512 workgroups, at least 128 columns a part (512 where
-// a wave takes a row of A by itself).
-int parts_of(const Ffn& f, int K) {
-  const int units = small_path(f) ? 1 : (f.T + 31) / 32, least = small_path(f) ? 512 : 128;
+// spread over the chip: 512 workgroups, at least 128 columns a part (512 by
+// waves).
+int parts_of(const Ffn& f, const Lora& l, int K) {
+  const bool waves = by_wave(f, l, K);
+  const int units = small_path(f) ? 1 : waves ? f.T : (f.T + 31) / 32, least = waves ? 512 : 128;
   int p = 512 / units;
   p = p < K / least ? p : K / least;
   return p < 1 ? 1 : p > kMaxParts ? kMaxParts : p;
 }
-
-// Tokens of a workgroup of the sort (8192 tokens in one workgroup: 8.4 us; 300: 3.9 us).
-constexpr int kPlanThreads = 1024, kPlanChunk = 8192;
-int plan_blocks(int T) { return (T + kPlanChunk - 1) / kPlanChunk; }
 
 struct Space {
   int32_t *perm, *sorted, *first, *hist;
@@ -63,7 +74,7 @@ Space space(const Ffn& f, const Lora& l, void* ws) {
   s.sorted = (int32_t*)take((size_t)f.T * 4);
   s.first = (int32_t*)take((size_t)(l.L + 2) * 4);
   s.hist = (int32_t*)take((size_t)plan_blocks(f.T) * (l.L + 1) * 4);
-  const int a = parts_of(f, f.H), b = parts_of(f, f.I);
+  const int a = parts_of(f, l, f.H), b = parts_of(f, l, f.I);
   s.v = (float*)take((size_t)(a > b ? a : b) * f.T * l.r * 4);
   s.bytes = at;
   return s;
@@ -109,9 +120,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count(const int32_t* ids, i
 // Every workgroup counts its chunk, finds its first position in every bin from
 // all chunks' counts (hist; a lone workgroup's are its own), and places its
 // tokens.  Block 0 writes the bins' first positions.
-__global__ __launch_bounds__(kPlanThreads) void plan_place(const int32_t* ids, int T, int L, int chunk,
-                                                           const int32_t* hist, int blocks, int32_t* perm,
-                                                           int32_t* sorted, int32_t* first) {
+__device__ __forceinline__ void place_tokens(const int32_t* ids, int T, int L, int chunk, const int32_t* hist,
+                                             int blocks, int32_t* perm, int32_t* sorted, int32_t* first) {
   __shared__ int start[kLoraMaxAdapters + 1];
   __shared__ int wave_sum[kPlanThreads / 64];
   __shared__ int carry;
@@ -169,6 +179,58 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place(const int32_t* ids, i
       perm[at] = t0 + q * kPlanThreads + threadIdx.x;
       sorted[at] = bin[q];
     }
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_place(const int32_t* ids, int T, int L, int chunk,
+                                                           const int32_t* hist, int blocks, int32_t* perm,
+                                                           int32_t* sorted, int32_t* first) {
+  place_tokens(ids, T, L, chunk, hist, blocks, perm, sorted, first);
+}
+
+// ---------------------------------------------------------------------------
+// Low-rank values by waves.
+
+// One row of A times x over the 8-column chunks c0 .. c1, by a wave.
+template <class E>
+__device__ __forceinline__ float low_rank_value(const E* x, const E* a, int c0, int c1, int lane) {
+  float s = 0.0f;
+#pragma unroll 4
+  for (int c = c0 + lane; c < c1; c += 64) {
+    tile::Vec8<E> p, q;
+    p.load(x + c * 8);
+    q.load(a + c * 8);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(p[e], q[e], s);
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
+  return s;
+}
+
+// v[part, t, j] = s_a A_a[j] . x[t] over a part of K: workgroups (token, part,
+// ranks by the number of waves).  PLAN: the first workgroup sorts the tokens
+// instead.
+template <class E, int WAVES, bool PLAN>
+__global__ __launch_bounds__(WAVES * 64, 8) void low_kernel(const E* x, const E* a, const float* scale,
+                                                         const int32_t* ids, int T, int K, int L, int r, int parts,
+                                                         float* v, int32_t* perm, int32_t* sorted, int32_t* first) {
+  static_assert(!PLAN || WAVES * 64 == kPlanThreads, "threads of the sort");
+  int block = blockIdx.x;
+  if constexpr (PLAN) {
+    if (block == 0) {
+      place_tokens(ids, T, L, T, nullptr, 1, perm, sorted, first);
+      return;
+    }
+    --block;
+  }
+  const int t = block % T, part = block / T % parts, lane = threadIdx.x & 63;
+  const int j = block / T / parts * WAVES + (threadIdx.x >> 6);
+  const int ad = ids[t];
+  if (ad < 0 || ad >= L || j >= r) return;
+  const int chunks = K / 8;
+  const int c0 = chunks * part / parts, c1 = chunks * (part + 1) / parts;
+  const float s = low_rank_value(x + (size_t)t * K, a + ((size_t)ad * r + j) * K, c0, c1, lane);
+  if (lane == 0) v[((size_t)part * T + t) * r + j] = s * scale[ad];
 }
 
 // ---------------------------------------------------------------------------
@@ -245,9 +307,10 @@ template <class E>
 struct AddLora {
   static constexpr bool ON = true, MAPPED = true;
   const int32_t *perm, *sorted, *first;
-  const float* v;  // [parts, T, r]
+  const float* v;  // [parts, T, r], by position or by token
   const E* b;      // [L, rows, r]
   int T, L, r, rows, parts;
+  bool by_token;
 
   __device__ __forceinline__ int a_row(int p) const { return perm[p]; }
   __device__ __forceinline__ int out_row(int p) const { return perm[p]; }
@@ -325,12 +388,14 @@ struct AddLora {
       for (int e = wave * 64 + lane; e < C::BM * 8; e += C::NTHR) {
         const int row = e >> 3, c = e & 7;
         f32x4 t[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        if (m0 + row < T && c * N < left)
+        if (m0 + row < T && c * N < left) {
+          const int at = by_token ? perm[m0 + row] : m0 + row;
           for (int s = 0; s < parts; ++s) {
-            const float* q = v + ((size_t)s * T + m0 + row) * r + k0 + c * N;
+            const float* q = v + ((size_t)s * T + at) * r + k0 + c * N;
 #pragma unroll
             for (int h = 0; h < N / 4; ++h) t[h] += reinterpret_cast<const f32x4*>(q)[h];
           }
+        }
         char* to = smem + row * 128 + (c ^ tile::swz_row<128>(row)) * 16;
         if constexpr (sizeof(E) == 2) {
           const uint2 a0 = pack_bf16x4(t[0]), a1 = pack_bf16x4(t[1]);
@@ -404,23 +469,51 @@ struct SwigluOut {
   }
 };
 
+hipError_t sort_tokens(const Ffn& f, const Lora& l, const int32_t* ids, const Space& s, hipStream_t st) {
+  const int blocks = plan_blocks(f.T), chunk = (f.T + blocks - 1) / blocks;
+  if (blocks > 1) {
+    hipLaunchKernelGGL(plan_count, dim3(blocks), dim3(kPlanThreads), 0, st, ids, f.T, l.L, chunk, s.hist);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(plan_place, dim3(blocks), dim3(kPlanThreads), 0, st, ids, f.T, l.L, chunk, s.hist, blocks,
+                     s.perm, s.sorted, s.first);
+  return hipGetLastError();
+}
+
+// plan: the tokens are not sorted yet.
 template <class E, class Epi>
 hipError_t big(const Ffn& f, const Lora& l, const void* x, int K, const void* w, int rows, const void* a,
-               const void* b, const float* scale, const Epi& epi, void* ws, hipStream_t st) {
+               const void* b, const float* scale, const int32_t* ids, bool plan, const Epi& epi, void* ws,
+               hipStream_t st) {
   const Space s = space(f, l, ws);
-  const int parts = parts_of(f, K);
-  const int units = (f.T + 31) / 32 + (l.L < f.T ? l.L : f.T);
-  auto shrink = [&](auto cfg) {
-    typedef decltype(cfg) C;
-    static_assert(C::BM == 32, "units of 32 tokens");
-    hipLaunchKernelGGL(shrink_kernel<C>, dim3(units, parts, (l.r + C::BN - 1) / C::BN), dim3(C::NTHR), 0, st,
-                       (const E*)x, (const E*)a, scale, s.perm, s.first, f.T, K, l.L, l.r, parts, s.v);
-    return hipGetLastError();
-  };
-  const hipError_t e = l.r <= 32 ? shrink(Cfg<E, 32, 32, 1, 2, 16, 128, 4, false, false>{})
-                                 : shrink(Cfg<E, 32, 64, 1, 4, 16, 128, 4, false, false>{});
+  const int parts = parts_of(f, l, K);
+  const bool waves = by_wave(f, l, K);
+  hipError_t e = hipSuccess;
+  if (waves) {
+    constexpr int W = kPlanThreads / 64;
+    auto low = [&](auto kernel, int before) {
+      hipLaunchKernelGGL(kernel, dim3(before + f.T * parts * ((l.r + W - 1) / W)), dim3(W * 64), 0, st, (const E*)x,
+                         (const E*)a, scale, ids, f.T, K, l.L, l.r, parts, s.v, s.perm, s.sorted, s.first);
+      return hipGetLastError();
+    };
+    e = plan ? low(low_kernel<E, W, true>, 1) : low(low_kernel<E, W, false>, 0);
+  } else {
+    if (plan) e = sort_tokens(f, l, ids, s, st);
+    if (e != hipSuccess) return e;
+    const int units = (f.T + 31) / 32 + (l.L < f.T ? l.L : f.T);
+    auto shrink = [&](auto cfg) {
+      typedef decltype(cfg) C;
+      static_assert(C::BM == 32, "units of 32 tokens");
+      hipLaunchKernelGGL(shrink_kernel<C>, dim3(units, parts, (l.r + C::BN - 1) / C::BN), dim3(C::NTHR), 0, st,
+                         (const E*)x, (const E*)a, scale, s.perm, s.first, f.T, K, l.L, l.r, parts, s.v);
+      return hipGetLastError();
+    };
+    e = l.r <= 32 ? shrink(Cfg<E, 32, 32, 1, 2, 16, 128, 4, false, false>{})
+                  : shrink(Cfg<E, 32, 64, 1, 4, 16, 128, 4, false, false>{});
+  }
   if (e != hipSuccess) return e;
-  const AddLora<E> add{s.perm, s.sorted, s.first, s.v, (const E*)b, f.T, l.L, l.r, rows, parts};
+  const AddLora<E> add{s.perm, s.sorted, s.first, s.v, (const E*)b, f.T, l.L, l.r, rows, parts, waves};
   const Operand A{x, K, f.T}, B{w, K, rows};
   const int half = Epi::PAIR ? rows / 2 : 0;
   return tile::run_product<E, false, false>(A, B, K, half, epi, st, add);
@@ -428,36 +521,6 @@ hipError_t big(const Ffn& f, const Lora& l, const void* x, int K, const void* w,
 
 // ---------------------------------------------------------------------------
 // Up to kSmallTokens tokens.
-
-// One row of A times x over the 8-column chunks c0 .. c1, by a wave.
-__device__ __forceinline__ float low_rank_value(const uint16_t* x, const uint16_t* a, int c0, int c1, int lane) {
-  float s = 0.0f;
-#pragma unroll 4
-  for (int c = c0 + lane; c < c1; c += 64) {
-    tile::Vec8<uint16_t> p, q;
-    p.load(x + c * 8);
-    q.load(a + c * 8);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) s = fmaf(p[e], q[e], s);
-  }
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) s += __shfl_xor(s, d);
-  return s;
-}
-
-// v[part, t, j] = s_a A_a[j] . x[t] over a part of K, a wave for each.
-__global__ __launch_bounds__(256) void shrink_small(const uint16_t* x, const uint16_t* a, const float* scale,
-                                                    const int32_t* ids, int T, int K, int L, int r, int parts,
-                                                    float* v) {
-  const int t = blockIdx.x, part = blockIdx.y, lane = threadIdx.x & 63;
-  const int j = blockIdx.z * 4 + (threadIdx.x >> 6);  // r is a multiple of 8
-  const int ad = ids[t];
-  if (ad < 0 || ad >= L) return;
-  const int chunks = K / 8;
-  const int c0 = chunks * part / parts, c1 = chunks * (part + 1) / parts;
-  const float s = low_rank_value(x + (size_t)t * K, a + ((size_t)ad * r + j) * K, c0, c1, lane);
-  if (lane == 0) v[((size_t)part * T + t) * r + j] = s * scale[ad];
-}
 
 // ROWS rows of W (PAIR: half of them gate rows, then their up rows), all
 // tokens: the waves split K in chunks of 64 columns, each with a ring of its
@@ -609,15 +672,16 @@ hipError_t small(const Ffn& f, const Lora& l, const void* x, int K, const void* 
                  const void* b, const float* scale, const int32_t* ids, const void* residual, void* out, void* ws,
                  hipStream_t st) {
   const Space s = space(f, l, ws);
-  const int parts = parts_of(f, K);
+  const int parts = parts_of(f, l, K);
   // Few low-rank values: every workgroup computes them for itself (two rows of A
   // a wave at most, from L2), which costs less than a launch.  One token,
   // rank 16, both projections: 12 us of kernels in two launches, 15 us in four (a
   // pass among others 16 and 24 us).
   const bool own = f.T * l.r <= 2 * kStreamWaves;
   if (!own) {
-    hipLaunchKernelGGL(shrink_small, dim3(f.T, parts, l.r / 4), dim3(256), 0, st, (const uint16_t*)x,
-                       (const uint16_t*)a, scale, ids, f.T, K, l.L, l.r, parts, s.v);
+    hipLaunchKernelGGL((low_kernel<uint16_t, 4, false>), dim3(f.T * parts * (l.r / 4)), dim3(256), 0, st,
+                       (const uint16_t*)x, (const uint16_t*)a, scale, ids, f.T, K, l.L, l.r, parts, s.v, s.perm,
+                       s.sorted, s.first);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -636,35 +700,23 @@ hipError_t small(const Ffn& f, const Lora& l, const void* x, int K, const void* 
 
 size_t lora_workspace_bytes(const Ffn& f, const Lora& l) { return space(f, l, nullptr).bytes; }
 
-hipError_t launch_lora_plan(const Ffn& f, const Lora& l, const int32_t* ids, void* ws, hipStream_t st) {
-  if (small_path(f)) return hipSuccess;
-  const Space s = space(f, l, ws);
-  const int blocks = plan_blocks(f.T), chunk = (f.T + blocks - 1) / blocks;
-  if (blocks > 1) {
-    hipLaunchKernelGGL(plan_count, dim3(blocks), dim3(kPlanThreads), 0, st, ids, f.T, l.L, chunk, s.hist);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(plan_place, dim3(blocks), dim3(kPlanThreads), 0, st, ids, f.T, l.L, chunk, s.hist, blocks,
-                     s.perm, s.sorted, s.first);
-  return hipGetLastError();
-}
-
 hipError_t launch_lora_w13(const Ffn& f, const Lora& l, const void* x, const void* w1, const void* a, const void* b,
                            const float* scale, const int32_t* ids, void* hs, void* ws, hipStream_t st) {
   if (small_path(f)) return small<true>(f, l, x, f.H, w1, 2 * f.I, a, b, scale, ids, nullptr, hs, ws, st);
-  if (f.bf16) return big<uint16_t>(f, l, x, f.H, w1, 2 * f.I, a, b, scale, SwigluOut<uint16_t>{(uint16_t*)hs, f.I}, ws, st);
-  return big<float>(f, l, x, f.H, w1, 2 * f.I, a, b, scale, SwigluOut<float>{(float*)hs, f.I}, ws, st);
+  if (f.bf16)
+    return big<uint16_t>(f, l, x, f.H, w1, 2 * f.I, a, b, scale, ids, true, SwigluOut<uint16_t>{(uint16_t*)hs, f.I},
+                         ws, st);
+  return big<float>(f, l, x, f.H, w1, 2 * f.I, a, b, scale, ids, true, SwigluOut<float>{(float*)hs, f.I}, ws, st);
 }
 
 hipError_t launch_lora_down(const Ffn& f, const Lora& l, const void* hs, const void* w2, const void* a, const void* b,
-                            const float* scale, const int32_t* ids, const void* residual, void* out, void* ws,
-                            hipStream_t st) {
+                            const float* scale, const int32_t* ids, bool sorted, const void* residual, void* out,
+                            void* ws, hipStream_t st) {
   if (small_path(f)) return small<false>(f, l, hs, f.I, w2, f.H, a, b, scale, ids, residual, out, ws, st);
   if (f.bf16)
-    return big<uint16_t>(f, l, hs, f.I, w2, f.H, a, b, scale,
+    return big<uint16_t>(f, l, hs, f.I, w2, f.H, a, b, scale, ids, !sorted,
                          tile::StoreOut<uint16_t>{(uint16_t*)out, (const uint16_t*)residual, f.H}, ws, st);
-  return big<float>(f, l, hs, f.I, w2, f.H, a, b, scale,
+  return big<float>(f, l, hs, f.I, w2, f.H, a, b, scale, ids, !sorted,
                     tile::StoreOut<float>{(float*)out, (const float*)residual, f.H}, ws, st);
 }
 

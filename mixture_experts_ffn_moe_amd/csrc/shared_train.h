@@ -37,12 +37,12 @@ struct Lora {
 };
 constexpr int kLoraMaxAdapters = 1024, kLoraMaxRank = 128;
 size_t lora_workspace_bytes(const Ffn& f, const Lora& l);
-// The adapters of T tokens, sorted, into the workspace (both products read it).
-hipError_t launch_lora_plan(const Ffn& f, const Lora& l, const int32_t* ids, void* ws, hipStream_t st);
+// launch_lora_w13 leaves the tokens sorted by adapter in the workspace;
+// `sorted`: launch_lora_down finds them so.
 hipError_t launch_lora_w13(const Ffn& f, const Lora& l, const void* x, const void* w1, const void* a, const void* b,
                            const float* scale, const int32_t* ids, void* hs, void* ws, hipStream_t st);
 hipError_t launch_lora_down(const Ffn& f, const Lora& l, const void* hs, const void* w2, const void* a, const void* b,
-                            const float* scale, const int32_t* ids, const void* residual, void* out, void* ws,
-                            hipStream_t st);
+                            const float* scale, const int32_t* ids, bool sorted, const void* residual, void* out,
+                            void* ws, hipStream_t st);
 
 }  // namespace moe

@@ -147,7 +147,6 @@ moe_status moe_lora_w13_swiglu(const moe_shape* shape, int32_t Is, const moe_lor
   MOE_CHECK(check_ptr(scale)); MOE_CHECK(check_ptr(adapter_ids)); MOE_CHECK(check_ptr(hs));
   MOE_CHECK(check_workspace(workspace, workspace_bytes, moe::lora_workspace_bytes(f, l)));
   hipStream_t st = (hipStream_t)stream;
-  MOE_CHECK(hip_status(moe::launch_lora_plan(f, l, adapter_ids, workspace, st)));
   return hip_status(moe::launch_lora_w13(f, l, x, w1s, a1, b1, scale, adapter_ids, hs, workspace, st));
 }
 
@@ -165,8 +164,7 @@ moe_status moe_lora_down(const moe_shape* shape, int32_t Is, const moe_lora_spec
   MOE_CHECK(check_ptr(out));
   MOE_CHECK(check_workspace(workspace, workspace_bytes, moe::lora_workspace_bytes(f, l)));
   hipStream_t st = (hipStream_t)stream;
-  MOE_CHECK(hip_status(moe::launch_lora_plan(f, l, adapter_ids, workspace, st)));
-  return hip_status(moe::launch_lora_down(f, l, hs, w2s, a2, b2, scale, adapter_ids, residual, out, workspace, st));
+  return hip_status(moe::launch_lora_down(f, l, hs, w2s, a2, b2, scale, adapter_ids, false, residual, out, workspace, st));
 }
 
 moe_status moe_shared_ffn_lora(const moe_shape* shape, int32_t Is, const moe_lora_spec* spec, const void* x,
@@ -184,9 +182,8 @@ moe_status moe_shared_ffn_lora(const moe_shape* shape, int32_t Is, const moe_lor
   MOE_CHECK(check_ptr(out));
   MOE_CHECK(check_workspace(workspace, workspace_bytes, moe::lora_workspace_bytes(f, l)));
   hipStream_t st = (hipStream_t)stream;
-  MOE_CHECK(hip_status(moe::launch_lora_plan(f, l, adapter_ids, workspace, st)));
   MOE_CHECK(hip_status(moe::launch_lora_w13(f, l, x, w1s, a1, b1, scale, adapter_ids, hs, workspace, st)));
-  return hip_status(moe::launch_lora_down(f, l, hs, w2s, a2, b2, scale, adapter_ids, residual, out, workspace, st));
+  return hip_status(moe::launch_lora_down(f, l, hs, w2s, a2, b2, scale, adapter_ids, true, residual, out, workspace, st));
 }
 
 }  // extern "C"

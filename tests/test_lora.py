@@ -121,6 +121,28 @@ def test_who_has_which_adapter(m, dev, kind, T, dtype):
     c.check()
 
 
+# 8192 low-rank values (T * r) of adapters of 65536 elements (r * K) are the most that are computed one by one
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,Is,r", [(64, 192, 96, 128), (65, 192, 96, 128), (341, 192, 96, 24), (342, 192, 96, 24),
+                                      (1024, 192, 96, 8), (1025, 192, 96, 8), (33, 512, 544, 128), (40, 576, 512, 128)])
+@pytest.mark.parametrize("kind", ["tokens", "runs"])
+def test_few_and_many_low_rank_values(m, dev, kind, T, H, Is, r, dtype):
+    c = Call(m, T, H, Is, 7, r, dtype, kind)
+    c.both(m)
+    c.check()
+    first = c.hs.clone(), c.out.clone()
+    c.out.fill_(float("nan"))
+    c.down(m)
+    assert torch.equal(c.out, first[1])
+    mine = c.d["ids"] != 2
+    for k in ("a1", "b1", "a2", "b2"):
+        c.d[k][2] = float("nan")
+    c.d["x"][~mine] = float("inf")
+    c.both(m)
+    assert torch.equal(c.hs[mine], first[0][mine]) and torch.equal(c.out[mine], first[1][mine])
+
+
 @pytest.mark.gpu
 def test_many_tokens_in_the_plan(m, dev):
     """More tokens than one workgroup sorts."""

@@ -244,6 +244,8 @@ struct Gather {
   const int32_t* perm;
   __device__ __forceinline__ int a_row(int p) const { return perm[p]; }
   __device__ __forceinline__ int out_row(int p) const { return p; }
+  template <class C, class R0, class Row>
+  __device__ __forceinline__ int begin(int, int, R0, Row, int, int) const { return 0; }
 };
 struct StoreLow {
   static constexpr bool PAIR = false;
@@ -327,8 +329,142 @@ struct AddLora {
     __shared__ Runs<BM> s;
     return s;
   }
+  // Ranks of one substep in tiles of 16-row fragments: a wave reads the fragments
+  // of B of its own rows' adapters straight from memory (16 short rows of B lie
+  // together), the first ones ahead of the main loop, and needs neither LDS
+  // nor barriers for them.  w13 of 300 tokens, K = 4096, rank 16, this way and
+  // by the ring: 64 adapters 17.7 and 20.6 us, 300 adapters 18.7 and 28, one 17.1
+  // and 17.1, none 17.4 and 15.6.
   template <class C>
-  __device__ __forceinline__ void begin(int m0, int wave, int lane) const {
+  static __device__ __forceinline__ constexpr bool direct(int r) {
+    return C::F == 16 && r <= C::M::SUB;
+  }
+  template <class C>
+  struct Ahead {
+    static constexpr int Q = C::FM < 4 ? 4 / C::FM : 1;  // adapters of a batch
+    static constexpr int N = 16 / sizeof(E);
+    int ad[C::FM], at[C::FM];   // of this lane's row: its adapter, its low-rank values
+    uint32_t heads[C::FM];      // fragment rows where another adapter begins
+    f32x4 low[C::FM][N / 4];    // the first part's values
+    int id[C::FM][Q];           // the first adapters
+    typename C::M::frag b[C::FM][Q][C::FN];
+  };
+  // The fragments of B of the next adapters among a fragment's rows.
+  template <class C, class R0, class Row>
+  __device__ __forceinline__ void take(uint32_t& heads, int ad, int (&id)[Ahead<C>::Q],
+                                       typename C::M::frag (&f)[Ahead<C>::Q][C::FN], R0 b_r0, Row brow, int lane) const {
+    const int k = Ahead<C>::N * (lane / 16);
+#pragma unroll
+    for (int q = 0; q < Ahead<C>::Q; ++q) {
+      id[q] = -1;
+#pragma unroll
+      for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int e = 0; e < Ahead<C>::N; ++e) f[q][j][e] = 0.0f;
+      if (heads == 0) continue;
+      id[q] = __builtin_amdgcn_readlane(ad, __ffs((int)heads) - 1);
+      heads &= heads - 1;
+      const E* base = uniform_ptr(b + (size_t)id[q] * rows * r);
+      if (k < r)
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+          f[q][j] = *reinterpret_cast<const typename C::M::frag*>(base + (size_t)brow(b_r0(j) + lane % 16) * r + k);
+    }
+  }
+
+  // Behind the first copies, ahead of the main loop.
+  template <class C, class R0, class Row>
+  __device__ __forceinline__ auto begin(int m0, int wave_m, R0 b_r0, Row brow, int wave, int lane) const {
+    if constexpr (C::F == 16) {
+      Ahead<C> h;
+      if (!direct<C>(r)) {
+        list_runs<C>(m0, wave, lane);
+        return h;
+      }
+      const int k = Ahead<C>::N * (lane / 16);
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        const int p = m0 + wave_m + 16 * i + lane % 16;
+        h.ad[i] = p < T ? sorted[p] : L;
+        h.at[i] = p < T && by_token ? perm[p] : p;
+      }
+#pragma unroll
+      for (int i = 0; i < C::FM; ++i) {
+        const int left = __shfl_up(h.ad[i], 1);
+        h.heads[i] = (uint32_t)__ballot(h.ad[i] < L && (lane == 0 || h.ad[i] != left)) & 0xffffu;
+        take<C>(h.heads[i], h.ad[i], h.id[i], h.b[i], b_r0, brow, lane);
+#pragma unroll
+        for (int c = 0; c < Ahead<C>::N / 4; ++c) {
+          h.low[i][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if (h.ad[i] < L && k < r) h.low[i][c] = reinterpret_cast<const f32x4*>(v + (size_t)h.at[i] * r + k)[c];
+        }
+      }
+      return h;
+    } else {
+      list_runs<C>(m0, wave, lane);
+      return 0;
+    }
+  }
+
+  template <class C, class R0, class Row>
+  __device__ __forceinline__ void add_direct(typename C::M::acc (&acc)[C::FM][C::FN], const Ahead<C>& h, R0 b_r0, Row brow,
+                                             int lane) const {
+    constexpr int N = Ahead<C>::N, Q = Ahead<C>::Q;
+    const int k = N * (lane / 16);
+#pragma unroll
+    for (int i = 0; i < C::FM; ++i) {
+      if (h.id[i][0] < 0) continue;  // no adapter in these rows
+      f32x4 t[N / 4];
+#pragma unroll
+      for (int c = 0; c < N / 4; ++c) t[c] = h.low[i][c];
+      if (h.ad[i] < L && k < r)
+        for (int s = 1; s < parts; ++s)
+#pragma unroll
+          for (int c = 0; c < N / 4; ++c)
+            t[c] += reinterpret_cast<const f32x4*>(v + ((size_t)s * T + h.at[i]) * r + k)[c];
+      typename C::M::frag value, rest;
+#pragma unroll
+      for (int e = 0; e < N; ++e) value[e] = t[e / 4][e % 4];
+      if constexpr (sizeof(E) == 2) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) rest[e] = t[e / 4][e % 4] - (float)value[e];
+      }
+      uint32_t heads = h.heads[i];
+      int id[Q];
+      typename C::M::frag f[Q][C::FN];
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        id[q] = h.id[i][q];
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j) f[q][j] = h.b[i][q][j];
+      }
+      for (;;) {
+        typename C::M::acc d[Q][C::FN];
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j) {
+            d[q][j] = typename C::M::acc{0.f, 0.f, 0.f, 0.f};
+            if constexpr (sizeof(E) == 2) d[q][j] = C::M::mul(f[q][j], rest, d[q][j]);
+            d[q][j] = C::M::mul(f[q][j], value, d[q][j]);
+          }
+        tile::settle();
+        // every lane holds one row: it takes the product of its own adapter
+#pragma unroll
+        for (int q = 0; q < Q; ++q)
+#pragma unroll
+          for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][j][e] = h.ad[i] == id[q] ? acc[i][j][e] + d[q][j][e] : acc[i][j][e];
+        if (heads == 0) break;
+        take<C>(heads, h.ad[i], id, f, b_r0, brow, lane);
+      }
+    }
+  }
+
+  // Where not direct: the tile's runs, for add.
+  template <class C>
+  __device__ __forceinline__ void list_runs(int m0, int wave, int lane) const {
     if (wave != 0) return;
     Runs<C::BM>& s = runs<C::BM>();
     int n = 0;
@@ -350,16 +486,18 @@ struct AddLora {
     }
   }
 
-  // Adds B_a v to the tile's accumulators, the ring's LDS in use for it: the
+  // Adds B_a v to the tile's accumulators; where not direct, with the ring's LDS in use for it: the
   // tile's low-rank values of RS ranks (summed over the parts), and a ring of
   // the B rows of the tile's adapters, copied ahead.  In bf16 a low-rank value is
   // the sum of two operands, its rounding and the rounding of what is left:
   // rounded once it raised the error of SwiGLU's output from 1.7e-3 (its own
   // rounding) to 3.1e-3 where the adapters' part is large.  b_r0(j): first tile row of this
   // wave's fragment j; brow(i): row of B of tile row i.
-  template <class C, class R0, class Row>
-  __device__ __forceinline__ void add(typename C::M::acc (&acc)[C::FM][C::FN], char* smem, int m0, int wave_m, R0 b_r0,
-                                      Row brow, int wave, int lane) const {
+  template <class C, class H, class R0, class Row>
+  __device__ __forceinline__ void add(typename C::M::acc (&acc)[C::FM][C::FN], const H& ahead, char* smem, int m0,
+                                      int wave_m, R0 b_r0, Row brow, int wave, int lane) const {
+    if constexpr (C::F == 16)
+      if (direct<C>(r)) return add_direct<C>(acc, ahead, b_r0, brow, lane);
     typedef Cfg<E, C::BM, C::BN, C::WM, C::WN, C::F, 128, 2, false, false> S;  // tiles of 128-byte rows
     constexpr int RS = 128 / sizeof(E), V_BYTES = sizeof(E) == 2 ? 2 * S::A_BYTES : S::A_BYTES;
     constexpr int RING = (C::LDS_BYTES - V_BYTES) / S::B_BYTES < 6 ? (C::LDS_BYTES - V_BYTES) / S::B_BYTES : 6;

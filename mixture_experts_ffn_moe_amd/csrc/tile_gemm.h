@@ -226,6 +226,8 @@ struct NoExtra {
   static constexpr bool ON = false, MAPPED = false;
   __device__ __forceinline__ int a_row(int r) const { return r; }
   __device__ __forceinline__ int out_row(int r) const { return r; }
+  template <class C, class R0, class Row>
+  __device__ __forceinline__ int begin(int, int, R0, Row, int, int) const { return 0; }
 };
 
 // One tile, from row m0 and column n0 on.  PAIR: B has two halves of `half`
@@ -307,7 +309,11 @@ __device__ __forceinline__ void product(const Operand A, const Operand B, int K,
       for (int i = 0; i < NI; ++i) copy_piece(i);
     }
   }
-  if constexpr (Extra::ON) extra.template begin<C>(m0, wave, lane);
+  auto all_row = [&](int r) {  // row of B, from its start, of tile row r
+    const int up = PAIR && r >= C::BN / 2;
+    return up * half + min(n0 + r - up * (C::BN / 2), N - 1);
+  };
+  [[maybe_unused]] const auto ahead = extra.template begin<C>(m0, wm * C::TM, b_r0, all_row, wave, lane);
   // The next k-tile has landed for every wave, and the slot of the one before it is free.
   auto landed = [&]() {
     wait_vmcnt<(C::SLOTS - 2) * NI>();
@@ -395,10 +401,7 @@ __device__ __forceinline__ void product(const Operand A, const Operand B, int K,
   wait_vmcnt<0>();  // copies that nothing waited for
   __syncthreads();  // every wave is past its last LDS read: the ring is free
   if constexpr (Extra::ON) {
-    extra.template add<C>(acc, smem, m0, wm * C::TM, b_r0, [&](int r) {
-      const int up = PAIR && r >= C::BN / 2;
-      return up * half + min(n0 + r - up * (C::BN / 2), N - 1);
-    }, wave, lane);
+    extra.template add<C>(acc, ahead, smem, m0, wm * C::TM, b_r0, all_row, wave, lane);
     settle();
     __syncthreads();
   }

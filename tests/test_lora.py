@@ -143,6 +143,17 @@ def test_few_and_many_low_rank_values(m, dev, kind, T, H, Is, r, dtype):
     assert torch.equal(c.hs[mine], first[0][mine]) and torch.equal(c.out[mine], first[1][mine])
 
 
+# about every row of a tile another adapter, in tiles of 64 rows and (fp32) 128, ranks of one matrix step and past it
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,Is,r", [(1000, 64, 800, 16), (1000, 64, 800, 32), (1000, 64, 800, 40), (500, 1024, 1056, 24),
+                                      (1000, 1024, 544, 8), (1200, 64, 1312, 16)])
+def test_many_adapters_in_a_tile(m, dev, T, H, Is, r, dtype):
+    c = Call(m, T, H, Is, 400, r, dtype, "tokens")
+    c.both(m)
+    c.check()
+
+
 @pytest.mark.gpu
 def test_many_tokens_in_the_plan(m, dev):
     """More tokens than one workgroup sorts."""

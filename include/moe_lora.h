@@ -24,7 +24,7 @@
  * rank); adapter_ids [T] int32.  One A serves gate and up; separate ones
  * are stacked (rank 2r, B with a block of zeros beside each).  Adapters of
  * lower rank are padded with zeros.  Sums are in fp32; in a bf16 layer of
- * more than 16 tokens scale * A x enters the second product as the sum of two
+ * more than 32 tokens scale * A x enters the second product as the sum of two
  * bf16 values (its rounding and the rounding of the rest, 2^-16 off).
  *
  * Envelope, beside moe_mi355x.h's and moe_shared_train.h's for Is: rank a

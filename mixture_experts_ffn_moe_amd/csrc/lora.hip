@@ -27,7 +27,11 @@ using tile::Cfg;
 using tile::Mma;
 using tile::Operand;
 
-constexpr int kSmallTokens = 16;
+// Tokens up to which W is streamed.  32 tokens, H = 4096, Is = 768, both
+// projections in a graph, this way and by tiles (24 workgroups for w13): rank 16 of 64
+// adapters 19.0 and 34.3 us, rank 128 of 4 51.7 and 51.6.  64 tokens, 8 rows of W a
+// workgroup: rank 16 of 64 31.5 and 35.9, but H = 2048, Is = 1536, rank 32 39.3 and 29.3.
+constexpr int kSmallTokens = 32;
 constexpr int kMaxParts = 8;
 
 bool small_path(const Ffn& f) { return f.bf16 && f.T <= kSmallTokens; }
@@ -668,52 +672,54 @@ hipError_t big(const Ffn& f, const Lora& l, const void* x, int K, const void* w,
 // behind the first copies, so that the latencies overlap.  16 tokens, H = 4096,
 // Is = 768, rank 32: 7.1 us for w13 (12.6 MB of weights, 2.7 us at the copy rate; 13 us
 // with operands read straight from memory, 16 rows per 16 lanes) and 4.5 us down.
-constexpr int kStreamWaves = 16, kStreamRing = 2;
+// Above 16 tokens x takes twice the LDS of a slot, and half as many waves have
+// a ring each; a third slot in it changed nothing.
+constexpr int kStreamRing = 2;
+constexpr int stream_waves(int tokens) { return tokens == 16 ? 16 : 8; }
 
-// OWN: the low-rank values are computed here, by every workgroup for itself.
-template <bool PAIR, int ROWS, bool OWN>
-__global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(const uint16_t* x, const uint16_t* w,
-                                                                   const uint16_t* a, const uint16_t* b,
-                                                                   const float* scale, const int32_t* ids,
-                                                                   const float* v, const uint16_t* residual,
-                                                                   uint16_t* out, int T, int K, int N, int L, int r,
-                                                                   int parts) {
-  static_assert(ROWS == 8 || ROWS == 16, "rows of W");
-  constexpr int SLOT = (ROWS + 16) * 128, COPIES = ROWS / 8 + 2;
-  constexpr int RING = kStreamWaves * kStreamRing * SLOT;
+// TOK: the most tokens.  OWN: the low-rank values are computed here, by every
+// workgroup for itself.
+template <bool PAIR, int ROWS, int TOK, bool OWN>
+__global__ __launch_bounds__(stream_waves(TOK) * 64) void stream_kernel(
+    const uint16_t* x, const uint16_t* w, const uint16_t* a, const uint16_t* b, const float* scale, const int32_t* ids,
+    const float* v, const uint16_t* residual, uint16_t* out, int T, int K, int N, int L, int r, int parts) {
+  static_assert((ROWS == 8 || ROWS == 16) && (TOK == 16 || TOK == 32), "rows of W, tokens");
+  constexpr int WAVES = stream_waves(TOK), FR = TOK / 16, XG = TOK / 8, WG = ROWS / 8;
+  constexpr int SLOT = (ROWS + TOK) * 128, COPIES = WG + XG;
+  constexpr int RING = WAVES * kStreamRing * SLOT;
+  static_assert(TOK * ROWS <= WAVES * 64, "a thread for every result");
   __shared__ __attribute__((aligned(1024))) char ring[RING];
-  __shared__ float low[kSmallTokens * kLoraMaxRank];
+  __shared__ float low[TOK * kLoraMaxRank];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int half = N / 2, cols = PAIR ? ROWS / 2 : ROWS;
   const int n0 = blockIdx.x * cols;
   auto wrow = [&](int i) { return i < cols ? n0 + i : half + n0 + i - cols; };
   const int chunks = (K + 63) / 64;
   const uint32_t lds = (uint32_t)(uintptr_t)ring + (uint32_t)(wave * kStreamRing * SLOT);
-  uint32_t woff[ROWS / 8], xoff[2];
-  const int lr = lane >> 3;
-  int col[2];  // columns of this lane's 16 bytes, by row group
+  uint32_t woff[WG], xoff[XG];
+  int col[XG];  // columns of this lane's 16 bytes, by row group
 #pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const int row = g * 8 + lr;
+  for (int g = 0; g < XG; ++g) {
+    const int row = g * 8 + (lane >> 3);
     col[g] = ((lane & 7) ^ tile::swz_row<128>(row)) * 8;
-    if (g < ROWS / 8) woff[g] = ((uint32_t)wrow(row) * (uint32_t)K + (uint32_t)col[g]) * 2u;
+    if (g < WG) woff[g] = ((uint32_t)wrow(row) * (uint32_t)K + (uint32_t)col[g]) * 2u;
     xoff[g] = ((uint32_t)min(row, T - 1) * (uint32_t)K + (uint32_t)col[g]) * 2u;
   }
   // Copies of chunk c into slot c's place; the last chunk may hold 32 columns
   // only: what lies past them is read from the chunk's start and not used.
   auto copy = [&](int n) {
-    const int c = wave + kStreamWaves * n;
+    const int c = wave + WAVES * n;
     const bool past = c * 64 + 64 > K;
     const uint32_t s = lds + (uint32_t)((n % kStreamRing) * SLOT);
     const char* pw = uniform_ptr((const char*)w + (size_t)c * 128);
     const char* px = uniform_ptr((const char*)x + (size_t)c * 128);
 #pragma unroll
-    for (int g = 0; g < ROWS / 8; ++g) dma16(s + g * 1024u, pw, past && col[g] >= 32 ? woff[g] - col[g] * 2u : woff[g]);
+    for (int g = 0; g < WG; ++g) dma16(s + g * 1024u, pw, past && col[g] >= 32 ? woff[g] - col[g] * 2u : woff[g]);
 #pragma unroll
-    for (int g = 0; g < 2; ++g)
+    for (int g = 0; g < XG; ++g)
       dma16(s + ROWS * 128u + g * 1024u, px, past && col[g] >= 32 ? xoff[g] - col[g] * 2u : xoff[g]);
   };
-  const int mine = wave < chunks ? (chunks - wave + kStreamWaves - 1) / kStreamWaves : 0;
+  const int mine = wave < chunks ? (chunks - wave + WAVES - 1) / WAVES : 0;
 #pragma unroll
   for (int n = 0; n < kStreamRing; ++n)
     if (n < mine) copy(n);
@@ -730,7 +736,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(const uint16_
       if (c * 8 < r) q[c].load(pb + c * 8);
   }
   if constexpr (OWN) {
-    for (int e = wave; e < T * r; e += kStreamWaves) {
+    for (int e = wave; e < T * r; e += WAVES) {
       const int to = e / r, id = ids[to];
       if (id >= 0 && id < L) {
         const float s = low_rank_value(x + (size_t)to * K, a + ((size_t)id * r + e % r) * K, 0, K / 8, lane) * scale[id];
@@ -738,7 +744,7 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(const uint16_
       }
     }
   } else {
-    for (int e = tid; e < T * r; e += kStreamWaves * 64) {
+    for (int e = tid; e < T * r; e += WAVES * 64) {
       const int id = ids[e / r];
       float s = 0.0f;
       if (id >= 0 && id < L)
@@ -747,7 +753,9 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(const uint16_
     }
   }
 
-  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  f32x4 acc[FR];
+#pragma unroll
+  for (int f = 0; f < FR; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
   const int fr = lane & 15;
   for (int n = 0; n < mine; ++n) {
     // chunk n has landed; behind it at most one chunk's copies are in flight
@@ -757,13 +765,16 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(const uint16_
       wait_vmcnt<0>();
     __builtin_amdgcn_sched_barrier(0);
     const char* s = ring + wave * kStreamRing * SLOT + (n % kStreamRing) * SLOT;
-    const int steps = min(2, (K - (wave + kStreamWaves * n) * 64) / 32);
+    const int steps = min(2, (K - (wave + WAVES * n) * 64) / 32);
     for (int ks = 0; ks < steps; ++ks) {
-      const int c = ((ks * 4 + (lane >> 4)) ^ tile::swz_row<128>(fr)) * 16;
       const int wr = fr % ROWS, cw = ((ks * 4 + (lane >> 4)) ^ tile::swz_row<128>(wr)) * 16;
       const bf16x8 fw = *reinterpret_cast<const bf16x8*>(s + wr * 128 + cw);
-      const bf16x8 fx = *reinterpret_cast<const bf16x8*>(s + ROWS * 128 + fr * 128 + c);
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw, fx, acc, 0, 0, 0);
+#pragma unroll
+      for (int f = 0; f < FR; ++f) {
+        const int xr = f * 16 + fr, cx = ((ks * 4 + (lane >> 4)) ^ tile::swz_row<128>(xr)) * 16;
+        const bf16x8 fx = *reinterpret_cast<const bf16x8*>(s + ROWS * 128 + xr * 128 + cx);
+        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fw, fx, acc[f], 0, 0, 0);
+      }
     }
     if (n + kStreamRing < mine) {
       __builtin_amdgcn_s_waitcnt(0xF | (7 << 4) | (0 << 8) | (3 << 14));  // the slot's reads are done
@@ -775,13 +786,15 @@ __global__ __launch_bounds__(kStreamWaves * 64) void stream_kernel(const uint16_
   __syncthreads();  // every wave is past its ring
   // lane: token lane % 16, rows 4 * (lane / 16) + e
   float* sums = reinterpret_cast<float*>(ring);
-  static_assert(kStreamWaves * 16 * 20 * 4 <= RING, "sums in the ring's place");
-  *reinterpret_cast<f32x4*>(sums + (wave * 16 + fr) * 20 + 4 * (lane >> 4)) = acc;
+  static_assert(WAVES * TOK * 20 * 4 <= RING, "sums in the ring's place");
+#pragma unroll
+  for (int f = 0; f < FR; ++f)
+    *reinterpret_cast<f32x4*>(sums + (wave * TOK + f * 16 + fr) * 20 + 4 * (lane >> 4)) = acc[f];
   __syncthreads();
-  if (tid >= 16 * ROWS) return;
+  if (tid >= TOK * ROWS) return;
   float s = 0.0f;
   if (live)
-    for (int p = 0; p < kStreamWaves; ++p) s += sums[(p * 16 + t) * 20 + i];
+    for (int p = 0; p < WAVES; ++p) s += sums[(p * TOK + t) * 20 + i];
   if (has) {
     float d = 0.0f;
 #pragma unroll
@@ -815,7 +828,7 @@ hipError_t small(const Ffn& f, const Lora& l, const void* x, int K, const void* 
   // a wave at most, from L2), which costs less than a launch.  One token,
   // rank 16, both projections: 12 us of kernels in two launches, 15 us in four (a
   // pass among others 16 and 24 us).
-  const bool own = f.T * l.r <= 2 * kStreamWaves;
+  const bool own = f.T * l.r <= 2 * stream_waves(16);
   if (!own) {
     hipLaunchKernelGGL((low_kernel<uint16_t, 4, false>), dim3(f.T * parts * (l.r / 4)), dim3(256), 0, st,
                        (const uint16_t*)x, (const uint16_t*)a, scale, ids, f.T, K, l.L, l.r, parts, s.v, s.perm,
@@ -823,15 +836,19 @@ hipError_t small(const Ffn& f, const Lora& l, const void* x, int K, const void* 
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  auto stream = [&](auto kernel, int per) {
-    hipLaunchKernelGGL(kernel, dim3(rows / per), dim3(kStreamWaves * 64), 0, st, (const uint16_t*)x,
+  auto stream = [&](auto kernel, int per, int tokens) {
+    hipLaunchKernelGGL(kernel, dim3(rows / per), dim3(stream_waves(tokens) * 64), 0, st, (const uint16_t*)x,
                        (const uint16_t*)w, (const uint16_t*)a, (const uint16_t*)b, scale, ids, s.v,
                        (const uint16_t*)residual, (uint16_t*)out, f.T, K, rows, l.L, l.r, parts);
     return hipGetLastError();
   };
   // sixteen rows a workgroup leave CUs without one below 4096 rows
-  if (rows < 4096) return own ? stream(stream_kernel<PAIR, 8, true>, 8) : stream(stream_kernel<PAIR, 8, false>, 8);
-  return own ? stream(stream_kernel<PAIR, 16, true>, 16) : stream(stream_kernel<PAIR, 16, false>, 16);
+  auto by_rows = [&](auto per) {
+    constexpr int R = decltype(per)::value;
+    if (f.T > 16) return stream(stream_kernel<PAIR, R, 32, false>, R, 32);
+    return own ? stream(stream_kernel<PAIR, R, 16, true>, R, 16) : stream(stream_kernel<PAIR, R, 16, false>, R, 16);
+  };
+  return rows < 4096 ? by_rows(tile::Index<8>{}) : by_rows(tile::Index<16>{});
 }
 
 }  // namespace

@@ -154,6 +154,23 @@ def test_many_adapters_in_a_tile(m, dev, T, H, Is, r, dtype):
     c.check()
 
 
+# the token counts at which the kernels change, K short of a copied row, sixteen rows of W a workgroup
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [16, 17, 32, 33])
+@pytest.mark.parametrize("H,Is,r", [(320, 160, 8), (192, 96, 128), (4096, 32, 40), (64, 2080, 24)])
+def test_few_tokens(m, dev, T, H, Is, r):
+    c = Call(m, T, H, Is, 9, r, "bf16", "tokens")
+    c.both(m)
+    c.check()
+    first = c.hs.clone(), c.out.clone()
+    mine = c.d["ids"] != 2
+    for k in ("a1", "b1", "a2", "b2"):
+        c.d[k][2] = float("nan")
+    c.d["x"][~mine] = float("inf")
+    c.both(m)
+    assert torch.equal(c.hs[mine], first[0][mine]) and torch.equal(c.out[mine], first[1][mine])
+
+
 @pytest.mark.gpu
 def test_many_tokens_in_the_plan(m, dev):
     """More tokens than one workgroup sorts."""

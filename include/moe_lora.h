@@ -49,7 +49,7 @@ typedef struct {
   int32_t rank;
 } moe_lora_spec;
 
-/* Workspace bytes of the calls below, or 0 if an argument is invalid or
+/* Workspace bytes of the calls below (never fewer for more tokens), or 0 if an argument is invalid or
  * unsupported.  Pure host function. */
 size_t moe_lora_workspace_size(const moe_shape* shape, int32_t Is, const moe_lora_spec* spec);
 

@@ -78,8 +78,11 @@ Space space(const Ffn& f, const Lora& l, void* ws) {
   s.sorted = (int32_t*)take((size_t)f.T * 4);
   s.first = (int32_t*)take((size_t)(l.L + 2) * 4);
   s.hist = (int32_t*)take((size_t)plan_blocks(f.T) * (l.L + 1) * 4);
-  const int a = parts_of(f, l, f.H), b = parts_of(f, l, f.I);
-  s.v = (float*)take((size_t)(a > b ? a : b) * f.T * l.r * 4);
+  // parts * T is at most this (512 workgroups of 32 tokens), which grows with T:
+  // a workspace for many tokens serves fewer
+  const size_t few = (size_t)f.T * kMaxParts;
+  const size_t low = few < 512 * 32 ? few : 512 * 32;
+  s.v = (float*)take((low > (size_t)f.T ? low : (size_t)f.T) * l.r * 4);
   s.bytes = at;
   return s;
 }

@@ -289,6 +289,14 @@ def test_refusals(m):
     assert m.moe_lora_workspace_size(m.make_shape(0, 64, 1, 1, 32, 1, "bf16"), 64, spec) > 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_workspace_grows_with_the_tokens(m, dtype):
+    for H, Is, L, r in ((4096, 768, 64, 16), (64, 32, 3, 128), (2048, 2048, 1000, 8)):
+        sizes = [m.moe_lora_workspace_size(m.make_shape(T, H, 1, 1, 32, 1, dtype), Is, m.make_lora(L, r))
+                 for T in [*range(1, 1200), *range(1200, 40000, 321)]]
+        assert all(0 < a <= b for a, b in zip(sizes, sizes[1:]))
+
+
 def test_binding_refuses_wrong_tensors(m):
     s, spec = m.make_shape(8, 64, 1, 1, 32, 1, "bf16"), m.make_lora(4, 16)
     t = torch.zeros(8, 64, dtype=torch.bfloat16)

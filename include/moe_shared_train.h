@@ -77,9 +77,10 @@ size_t moe_shared_backward_workspace_size(const moe_shape* shape, int32_t Is);
  * in dtype, rounded once from fp32 sums over operands in dtype (dg and du are
  * rounded to dtype).  Every element of an output is written (gradients are
  * not added to).  d_x may be NULL (not wanted: w1s may then be NULL too);
- * d_w1s and d_w2s may both be NULL (then x and hs may be NULL); not all three.
- * Rows of padding: finite x with d_out of zero leaves the weights'
- * gradients untouched.  T == 0 writes zeros to d_w1s and d_w2s.
+ * d_w1s and d_w2s may both be NULL (then x and hs may be NULL); not all three
+ * where there are tokens.  Rows of padding: finite x with d_out of zero leaves
+ * the weights' gradients untouched.  T == 0 writes zeros to d_w1s and d_w2s (NULL:
+ * enqueues nothing).
  *   workspace: moe_shared_backward_workspace_size bytes, 256-byte aligned. */
 moe_status moe_shared_ffn_backward(const moe_shape* shape, int32_t Is, double p,
                                    const uint64_t* rng, const void* x, const void* w1s,

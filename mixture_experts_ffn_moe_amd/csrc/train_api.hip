@@ -114,7 +114,9 @@ moe_status moe_shared_ffn_backward(const moe_shape* shape, int32_t Is, double p,
   Dropout d;
   MOE_CHECK(check_ffn(shape, Is, &f));
   MOE_CHECK(check_dropout(p, rng, &d));
-  if ((d_w1s == nullptr) != (d_w2s == nullptr) || (d_x == nullptr && d_w1s == nullptr)) return MOE_ERR_INVALID_ARG;
+  // an empty batch's d_x has no elements, and may have no address either
+  if ((d_w1s == nullptr) != (d_w2s == nullptr) || (f.T > 0 && d_x == nullptr && d_w1s == nullptr))
+    return MOE_ERR_INVALID_ARG;
   MOE_CHECK(check_or_null(d_x)); MOE_CHECK(check_or_null(d_w1s)); MOE_CHECK(check_or_null(d_w2s));
   if (f.T > 0) {
     if (d_w1s) MOE_CHECK(check_ptr(x));

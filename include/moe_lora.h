@@ -25,7 +25,9 @@
  * are stacked (rank 2r, B with a block of zeros beside each).  Adapters of
  * lower rank are padded with zeros.  Sums are in fp32; in a bf16 layer of
  * more than 32 tokens scale * A x enters the second product as the sum of two
- * bf16 values (its rounding and the rounding of the rest, 2^-16 off).
+ * bf16 values (its rounding, at most bf16's largest number, and the rounding of
+ * the rest, 2^-16 off; where scale * A x is infinite the rest is, and B times
+ * it is what it is in fp32).
  *
  * Envelope, beside moe_mi355x.h's and moe_shared_train.h's for Is: rank a
  * multiple of 8 up to 128, up to 1024 adapters, T * max(H, Is) elements below

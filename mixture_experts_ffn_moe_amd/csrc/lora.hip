@@ -312,6 +312,12 @@ __global__ __launch_bounds__(C::NTHR) void shrink_kernel(const typename C::E* x,
 // ---------------------------------------------------------------------------
 // The low-rank addition to a tile's accumulators.
 
+// What the first of the two bf16 operands of a low-rank value t rounds.  Past
+// bf16's largest number that number is taken: the rest t - 0x1.fep127 is then
+// finite where t is, and infinite or NaN where t is (an infinite first operand
+// would leave inf - inf).
+__device__ __forceinline__ float first_part(float t) { return __builtin_amdgcn_fmed3f(t, -0x1.fep127f, 0x1.fep127f); }
+
 template <class E>
 struct AddLora {
   static constexpr bool ON = true, MAPPED = true;
@@ -431,7 +437,7 @@ struct AddLora {
             t[c] += reinterpret_cast<const f32x4*>(v + ((size_t)s * T + h.at[i]) * r + k)[c];
       typename C::M::frag value, rest;
 #pragma unroll
-      for (int e = 0; e < N; ++e) value[e] = t[e / 4][e % 4];
+      for (int e = 0; e < N; ++e) value[e] = sizeof(E) == 2 ? first_part(t[e / 4][e % 4]) : t[e / 4][e % 4];
       if constexpr (sizeof(E) == 2) {
 #pragma unroll
         for (int e = 0; e < N; ++e) rest[e] = t[e / 4][e % 4] - (float)value[e];
@@ -543,7 +549,10 @@ struct AddLora {
         }
         char* to = smem + row * 128 + (c ^ tile::swz_row<128>(row)) * 16;
         if constexpr (sizeof(E) == 2) {
-          const uint2 a0 = pack_bf16x4(t[0]), a1 = pack_bf16x4(t[1]);
+          f32x4 first[2];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) first[i >> 2][i & 3] = first_part(t[i >> 2][i & 3]);
+          const uint2 a0 = pack_bf16x4(first[0]), a1 = pack_bf16x4(first[1]);
           tile::Vec8<uint16_t> a;
           a.d = make_uint4(a0.x, a0.y, a1.x, a1.y);
           *reinterpret_cast<uint4*>(to) = a.d;

@@ -88,34 +88,11 @@ __global__ __launch_bounds__(CX::NTHR, 1) void gradients_kernel(Part x, Part w, 
   }
 }
 
-// Estimated ns until `n1` tiles of `a` ns and behind them `n2` of `b` ns are
-// done, every tile going to the place that is free first.
-long long makespan(long long n1, long long a, long long n2, long long b, long long places) {
-  // the places that hold one tile of the first kind more, and the others
-  const long long extra = n1 % places;
-  long long t_extra = (n1 / places + 1) * a, t = n1 / places * a;
-  while (n2 > 0) {
-    const bool e = extra > 0 && t_extra <= t;
-    (e ? t_extra : t) += b;
-    n2 -= e ? extra : places - extra;
-  }
-  return extra > 0 && t_extra > t ? t_extra : t;
-}
-
 // has_x, has_w: which of the two are wanted.
 template <class E, class Epi>
 hipError_t run_both(Part x, bool has_x, const Epi& epi_x, Part w, bool has_w, const tile::StoreOut<E>& epi_w,
                     hipStream_t st) {
-  const int size = tile::cheapest<E>([&](const tile::TileCost& c) {
-    auto tiles = [&](const Part& p, bool has) {
-      return has ? (long long)((p.A.count + c.bm - 1) / c.bm) * ((p.B.count + c.bn - 1) / c.bn) : 0;
-    };
-    const long long nx = tiles(x, has_x), nw = tiles(w, has_w), a_cu = (nx + nw + tile::kCus - 1) / tile::kCus;
-    const int resident = a_cu < 1 ? 1 : a_cu < c.resident ? (int)a_cu : c.resident;
-    auto ns = [&](const Part& p) { return tile::tile_ns(c, ((long long)p.K * sizeof(E) + 127) / 128, resident); };
-    return w.K > x.K ? makespan(nw, ns(w), nx, ns(x), tile::kCus * resident)
-                     : makespan(nx, ns(x), nw, ns(w), tile::kCus * resident);
-  });
+  const int size = tile::pair_tile<E>({has_x ? x.A.count : 0, x.B.count, x.K}, {has_w ? w.A.count : 0, w.B.count, w.K});
   return tile::with_tile<E>(size, [&](auto index) {
     typedef typename tile::TileCfg<E, decltype(index)::value, false, true>::type CX;
     typedef typename tile::TileCfg<E, decltype(index)::value, true, true>::type CW;

@@ -31,6 +31,7 @@
 #pragma once
 
 #include "moe_common.h"
+#include "tile_choice.h"
 
 namespace moe {
 namespace tile {
@@ -467,28 +468,7 @@ hipError_t launch_product(Operand A, Operand B, int K, int half, const Epi& epi,
   return hipGetLastError();
 }
 
-// The tile sizes a product may take, and what one costs: ns per 128 bytes of k
-// with 1, 2, ... workgroups on every CU (as many as LDS holds), measured at
-// K = 4096 (bf16, average of a product with both operands k-contiguous and
-// one with both k-rows) and 2048 (fp32), and ns a tile beside that.
-struct TileCost {
-  int bm, bn, resident;
-  int step[3];
-};
-template <class E>
-struct TileCosts;
-template <>
-struct TileCosts<uint16_t> {
-  static constexpr int COUNT = 6;
-  static constexpr TileCost C[COUNT] = {{32, 64, 3, {185, 290, 420}}, {64, 64, 2, {230, 400, 0}}, {64, 128, 1, {340, 0, 0}},
-                                        {128, 128, 1, {490, 0, 0}},   {128, 256, 1, {880, 0, 0}}, {256, 256, 1, {1630, 0, 0}}};
-};
-template <>
-struct TileCosts<float> {
-  static constexpr int COUNT = 4;
-  static constexpr TileCost C[COUNT] = {{32, 64, 3, {300, 540, 770}}, {64, 64, 2, {520, 980, 0}}, {64, 128, 1, {1000, 0, 0}},
-                                        {128, 128, 1, {1890, 0, 0}}};
-};
+// The tile sizes a product may take (tile_choice.h).
 template <class E, int I, bool TA, bool TB>
 struct TileCfg;
 template <bool TA, bool TB> struct TileCfg<uint16_t, 0, TA, TB> { typedef Cfg<uint16_t, 32, 64, 2, 2, 16, 128, 4, TA, TB> type; };
@@ -499,52 +479,24 @@ template <bool TA, bool TB> struct TileCfg<uint16_t, 4, TA, TB> { typedef Cfg<ui
 template <bool TA, bool TB> struct TileCfg<uint16_t, 5, TA, TB> { typedef Cfg<uint16_t, 256, 256, 2, 4, 32, 64, 4, TA, TB> type; };
 template <bool TA, bool TB> struct TileCfg<float, 0, TA, TB> { typedef Cfg<float, 32, 64, 2, 2, 16, 128, 4, TA, TB> type; };
 template <bool TA, bool TB> struct TileCfg<float, 1, TA, TB> { typedef Cfg<float, 64, 64, 4, 2, 16, 128, 4, TA, TB> type; };
-template <bool TA, bool TB> struct TileCfg<float, 2, TA, TB> { typedef Cfg<float, 64, 128, 2, 4, 16, 128, 4, TA, TB> type; };
-template <bool TA, bool TB> struct TileCfg<float, 3, TA, TB> { typedef Cfg<float, 128, 128, 2, 4, 16, 128, 4, TA, TB> type; };
+template <bool TA, bool TB> struct TileCfg<float, 2, TA, TB> { typedef Cfg<float, 128, 128, 2, 4, 16, 128, 4, TA, TB> type; };
 
-inline long long tile_ns(const TileCost& c, long long steps, int resident) {
-  return steps * c.step[resident - 1] + 2200 + c.bm * c.bn / 8;
-}
-constexpr int kCus = 256;
-// Estimated ns of an M x N product: whole rounds of `resident` tiles a CU, and
-// what is left.
-inline long long product_ns(const TileCost& c, long long M, long long N, long long steps) {
-  const long long tiles = ((M + c.bm - 1) / c.bm) * ((N + c.bn - 1) / c.bn), a_cu = (tiles + kCus - 1) / kCus;
-  const int left = (int)(a_cu % c.resident);
-  return a_cu / c.resident * tile_ns(c, steps, c.resident) + (left ? tile_ns(c, steps, left) : 0);
-}
-template <class E, class F>
-int cheapest(F ns) {
-  int best = 0;
-  for (int i = 1; i < TileCosts<E>::COUNT; ++i)
-    if (ns(TileCosts<E>::C[i]) < ns(TileCosts<E>::C[best])) best = i;
-  return best;
-}
 // f(index constant) for tile size i.
 template <int I>
 struct Index {
   static constexpr int value = I;
 };
-template <class E, class F>
+template <class E, int I = 0, class F>
 hipError_t with_tile(int i, F f) {
-  switch (i) {
-    case 0: return f(Index<0>{});
-    case 1: return f(Index<1>{});
-    case 2: return f(Index<2>{});
-    default: break;
-  }
-  if constexpr (TileCosts<E>::COUNT > 4) {
-    if (i == 4) return f(Index<4>{});
-    if (i == 5) return f(Index<5>{});
-  }
-  return f(Index<3>{});
+  if constexpr (I + 1 < TileCosts<E>::COUNT)
+    if (i != I) return with_tile<E, I + 1>(i, f);
+  return f(Index<I>{});
 }
 // The product with the tile size that is estimated to be the fastest.
 template <class E, bool TA, bool TB, class Epi, class Extra = NoExtra>
 hipError_t run_product(const Operand& A, const Operand& B, int K, int half, const Epi& epi, hipStream_t st,
                        const Extra& extra = Extra{}) {
-  const long long N = Epi::PAIR ? 2ll * half : B.count, steps = ((long long)K * sizeof(E) + 127) / 128;
-  const int i = cheapest<E>([&](const TileCost& c) { return product_ns(c, A.count, N, steps); });
+  const int i = product_tile<E>(A.count, Epi::PAIR ? 2ll * half : B.count, K);
   return with_tile<E>(i, [&](auto index) {
     return launch_product<typename TileCfg<E, decltype(index)::value, TA, TB>::type>(A, B, K, half, epi, st, extra);
   });

@@ -89,7 +89,7 @@ class Call:
 
 
 # (T, H, Is, L, r): both sides of the small path's last token count, ranks within and past a matrix step, adapters
-# that share a row fragment, tokens enough for every tile size
+# that share a row fragment, tokens enough for larger tiles (every tile size: test_tile_sizes.py)
 SIZES = [(1, 64, 32, 1, 8), (2, 192, 96, 3, 24), (8, 4096, 768, 64, 16), (15, 320, 160, 4, 128), (16, 2048, 544, 70, 40),
          (17, 64, 32, 5, 8), (31, 192, 96, 7, 16), (33, 448, 160, 40, 24), (77, 256, 128, 3, 64), (130, 1280, 352, 9, 40),
          (300, 512, 288, 64, 16), (257, 64, 64, 2, 128), (1100, 2048, 1056, 12, 32), (6200, 64, 1056, 30, 72),

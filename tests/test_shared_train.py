@@ -84,8 +84,8 @@ class Step:
             assert torch.isnan(b[:256]).all() and torch.isnan(b[-256:]).all(), n
 
 
-# (T, H, Is): one token, rows and columns short of a tile, T around the k-tiles of the weights' gradients, and sizes
-# at which each product takes each of its tiles
+# (T, H, Is): one token, rows and columns short of a tile, T around the k-tiles of the weights' gradients, and larger
+# ones (every launch at every tile size: test_tile_sizes.py)
 SIZES = [(1, 64, 32), (2, 192, 96), (15, 64, 64), (63, 128, 32), (64, 256, 128), (65, 64, 160), (127, 320, 96),
          (129, 448, 224), (333, 1024, 352), (700, 1280, 1056), (6200, 64, 1056), (6200, 2048, 96), (33, 3008, 2080)]
 

@@ -76,7 +76,7 @@ Space space(const Ffn& f, const Lora& l, void* ws) {
   Space s;
   s.perm = (int32_t*)take((size_t)f.T * 4);
   s.sorted = (int32_t*)take((size_t)f.T * 4);
-  s.first = (int32_t*)take((size_t)(l.L + 2) * 4);
+  s.first = (int32_t*)take((size_t)(l.L + 1) * 4);
   s.hist = (int32_t*)take((size_t)plan_blocks(f.T) * (l.L + 1) * 4);
   // parts * T is at most this (512 workgroups of 32 tokens), which grows with T:
   // a workspace for many tokens serves fewer
@@ -178,7 +178,6 @@ __device__ __forceinline__ void place_tokens(const int32_t* ids, int T, int L, i
     if (threadIdx.x == kPlanThreads - 1) carry = base + incl;
     __syncthreads();
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) first[L + 1] = T;
 #pragma unroll
   for (int q = 0; q < KEEP; ++q)
     if (bin[q] >= 0) {

@@ -41,10 +41,18 @@ constexpr int kPlanThreads = 1024, kPlanChunk = 8192;
 int plan_blocks(int T) { return (T + kPlanChunk - 1) / kPlanChunk; }
 
 // Few low-rank values of short adapters are computed by a wave each: every wave
-// reads a row of A, from L2 mostly.  bf16, K = 4096, rank 16, a call of w13 by
-// waves and by tiles: 300 tokens 30.0 and 31.8 us (7.8 to 8.3 us with the sort in the
-// same launch; 4.8 and 5.3 in two), 512 tokens 36.0 and 39.0, 768 tokens 41.9 and 38.5;
-// rank 64, 128 tokens: 32.5 and 28.3.  fp32, K = 448, rank 8, 77 tokens: 13.2 and 18.5.
+// reads a row of A, from L2 mostly.  us of a call of w13 (N = 1536, bf16, in a graph)
+// by waves and by tiles, on both sides of either border:
+//   values (T r <= 8192): K = 4096, rank 16, 300 tokens 24.0 and 27.5, 512 29.6 and 33.6,
+//     768 40.0 and 38.5; rank 8, 1024 tokens 36.0 and 38.2, 1500 52.6 and 57.5; K = 1024,
+//     N = 512, rank 64, 100 tokens 16.0 and 17.9, 200 18.1 and 16.9;
+//   elements of an adapter (r K <= 65536), there: K = 8192, rank 8, 300 tokens 38.3 and
+//     40.7, 1024 61.6 and 56.6; 98304: K = 4096, rank 24, 128 tokens 25.8 and 27.8, 341 33.3
+//     and 34.3; 131072: K = 4096, rank 32, 256 tokens 28.7 and 29.2, K = 8192, rank 16, 300
+//     42.9 and 42.3, K = 16384, rank 8, 300 67.3 and 65.1, 1024 108 and 93; 262144: K = 4096,
+//     rank 64, 64 tokens 40.8 and 39.3; 524288: rank 128, 40 tokens 42.7 and 34.5.
+// fp32, K = 448, N = 320, rank 8, 77 tokens: 11.8 and 16.4; K = 4096, rank 16, 256 tokens: 56.5 and 60.7.
+// The sort's launch with 300 tokens' values of rank 16 takes 7.8 to 8.3 us (in two: 4.8 and 5.3).
 bool by_wave(const Ffn& f, const Lora& l, int K) {
   return small_path(f) || (f.T <= kPlanChunk && (long long)f.T * l.r <= 8192 && (long long)l.r * K <= 1 << 16);
 }
@@ -548,10 +556,10 @@ struct AddLora {
         }
         char* to = smem + row * 128 + (c ^ tile::swz_row<128>(row)) * 16;
         if constexpr (sizeof(E) == 2) {
-          f32x4 first[2];
+          f32x4 near[2];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) first[i >> 2][i & 3] = first_part(t[i >> 2][i & 3]);
-          const uint2 a0 = pack_bf16x4(first[0]), a1 = pack_bf16x4(first[1]);
+          for (int i = 0; i < 8; ++i) near[i >> 2][i & 3] = first_part(t[i >> 2][i & 3]);
+          const uint2 a0 = pack_bf16x4(near[0]), a1 = pack_bf16x4(near[1]);
           tile::Vec8<uint16_t> a;
           a.d = make_uint4(a0.x, a0.y, a1.x, a1.y);
           *reinterpret_cast<uint4*>(to) = a.d;

@@ -30,8 +30,7 @@ hipError_t launch_train_backward(const Ffn& f, const Dropout& d, const void* x, 
 hipError_t launch_dropout(bool bf16, const Dropout& d, long long n, const void* y, const void* residual, void* out,
                           hipStream_t st);
 
-// Low-rank adapters: L of rank r, the partial sums of the low-rank values in
-// `parts` parts of K.
+// Low-rank adapters: L of rank r.
 struct Lora {
   int L, r;
 };

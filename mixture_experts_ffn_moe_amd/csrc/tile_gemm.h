@@ -126,7 +126,7 @@ __device__ __forceinline__ int swz_k(int k) {
 // Source byte offsets of a wave's direct copies of one operand tile, relative
 // to the tile's base (the first row's, k-rows: first column's, at the current
 // k-tile).  C rows or columns from `first`, at most `count` of them exist.
-// `map` (may be null): stored row of a logical row.
+// row_of: stored row, relative to the base, of the tile's row (not for k-rows).
 // k_left: k-values from the k-tile's start to the end of K.
 template <class C, bool KROWS, int N, int Q, class Row>
 __device__ __forceinline__ void copy_offsets(uint32_t (&off)[Q], int first, int count, int ld, int k_left,
@@ -212,8 +212,8 @@ __device__ __forceinline__ void settle() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// Tile t of mt x nt: tiles run down groups of 8 row tiles, so that the 32
-// tiles a die works on at a time share their rows and columns in its L2.
+// Tile t of mt x nt: tiles run down groups of four row tiles, so that the 32
+// tiles a die works on at a time (4 x 8) share their rows and columns in its L2.
 __device__ __forceinline__ void tile_of(int t, int mt, int nt, int& m, int& n) {
   constexpr int G = 4;
   const int group = t / (G * nt), in = t - group * (G * nt);
